@@ -425,6 +425,155 @@ kvm_status kvm_score_select_static(const kvm_config *cfg, const void *q, int32_t
  */
 kvm_status kvm_score_select_static_status(kvm_stream stream);
 
+/*
+ * ---- The calls around the recall of one layer's attention: queries and keys
+ * normalised and rotated (kvm_qk_norm_rope), keys and values appended to a
+ * paged cache (kvm_append_kv), attention over the paged cache (kvm_attend), and
+ * the Mean-K index of 8-bit pages that carry scales (kvm_build_index_scaled).
+ *
+ * Paged cache.  K and V pages have the layout of every page in this header,
+ * [page][layer][kv_head][32][d] in kv_dtype: a prefill's K pages, the page pool
+ * of kvm_step, or pages of the caller's own.  A page's row t holds one token;
+ * K is rotated at the position the caller chose, and attention reads it as is.
+ * KVM_E4M3 pages may carry scales: k_scale / v_scale hold one float32 for each
+ * (scale row, layer, kv head), and a page's values are its codes times its
+ * scale.  Scales are powers of two 2^e with -100 <= e <= 119 (kvm_append_kv
+ * writes such scales); another value raises the device error flag where a
+ * kernel reads it.  A page uses the scale row of its own number, or the one that
+ * kvm_batch's scale_rows names: with scale_rows = sel_ids, the view's pages use
+ * the scales of the history blocks they hold, and no scale moves.  Rotating K
+ * never changes a block's scale (see kvm_append_kv), so kvm_assemble_view,
+ * kvm_step and kvm_stage_out move and re-rotate scaled pages as they move pages
+ * at unit scale.
+ */
+typedef struct {
+    void *k_pages;        /* device [n_pages][L][G][32][d], kv_dtype            */
+    void *v_pages;        /* device [n_pages][L][G][32][d], kv_dtype            */
+    float *k_scale;       /* device [n_scale_rows][L][G], or NULL: unit scale   */
+    float *v_scale;       /* device [n_scale_rows][L][G]; NULL when k_scale is  */
+    int64_t n_pages;
+    int64_t n_scale_rows; /* 0 without scales                                  */
+} kvm_cache;
+
+/* A batch of sequences of different lengths.  Sequence s owns the token rows
+ * [q_start[s], q_start[s+1]) of a call's token buffers: its newest q_len =
+ * q_start[s+1] - q_start[s] tokens, whose logical indexes in the sequence are
+ * kv_len[s] - q_len .. kv_len[s] - 1.  Logical index t lives in page
+ * page_table[s][t / 32], row t mod 32.  The device arrays are read when the
+ * kernels run, so a captured call follows their contents at launch time; the
+ * host fields bound them.  A sequence with an entry out of its bounds (q_start
+ * not ascending or beyond n_tokens, q_len > max_q_len, kv_len < 0 or >
+ * max_kv_len), a page outside the cache or a scale row outside its array raises
+ * the device error flag; nothing is read or written out of range.  Token rows
+ * outside every sequence are left as they were. */
+typedef struct {
+    int32_t n_seqs;            /* 0 .. 1024                                     */
+    int32_t n_tokens;          /* rows of the token buffers                     */
+    int32_t max_q_len;         /* largest q_len of a sequence                   */
+    int32_t max_kv_len;        /* largest kv_len, <= 32 * table_stride          */
+    const int32_t *q_start;    /* device [n_seqs + 1]                           */
+    const int32_t *kv_len;     /* device [n_seqs]                               */
+    const int32_t *page_table; /* device [n_seqs][table_stride]                 */
+    const int32_t *scale_rows; /* device, as page_table; NULL: row = page       */
+    int64_t table_stride;
+} kvm_batch;
+
+/*
+ * Queries and keys normalised per head and rotated, in one pass.
+ *
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     over each head's d entries
+ *   free = y,   rot = R_p y                     p = positions[token]
+ *
+ * in float32, each output rounded once.  free is what kvm_score_select and
+ * kvm_step take as RoPE-free queries and kvm_append_kv as keys; rot is what
+ * kvm_attend takes as queries.
+ * positions  device int32 [n_tokens], each in [0, max_positions); a token out
+ *            of that range raises the device error flag and is skipped.
+ * q, k       device, q_dtype: token t's heads at q + t * q_stride elements, H
+ *            (G for k) heads of d; NULL leaves that side out (not both).  Bases
+ *            and strides are multiples of 16 bytes; a packed projection row is
+ *            passed by pointers into it.
+ * q_weight, k_weight   device [d], q_dtype; NULL: that side is rotated without
+ *            being normalised.
+ * q_free, q_rot   device, [n_tokens][H][d], q_dtype; k_free, k_rot the same
+ *            with G heads.  Each nullable, one per given side at least; an
+ *            output may be its own input when that is packed the same way.
+ * Errors: KVM_ERR_INVALID_ARG.  n_tokens == 0 does nothing.
+ */
+kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *positions,
+                            const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const void *q_weight, const void *k_weight, float eps, void *q_free,
+                            void *q_rot, void *k_free, void *k_rot, kvm_stream stream);
+
+/*
+ * Append a batch's newest tokens to one layer of a paged cache, K rotated on
+ * the way.  For token j of sequence s, at logical index t = kv_len - q_len + j:
+ *   K row = R_p k,  V row = v,  raw row = k     p = positions ? positions[row] : t
+ * (float32 rotation, one rounding to kv_dtype; e4m3 saturates to +-448).
+ * k, v       device, q_dtype: token row i at k + i * k_stride elements, G heads
+ *            of d; k is RoPE-free.  Bases and strides multiples of 16 bytes.
+ * positions  device int32 [n_tokens], or NULL; a token whose position is outside
+ *            [0, max_positions) raises the device error flag and is skipped.
+ * raw_k_pages  nullable, device, as cache->k_pages: the same rows of raw K.
+ * Scaled e4m3 pages: a block's scale is the least 2^e (-100 <= e <= 119) with
+ * amax|k| <= 316.75 * 2^e, or amax|v| <= 448 * 2^e, over the finite entries of
+ * the rows this call writes, and never less than the block's scale so far
+ * unless the run begins at the block's row 0 (the block starts anew).  316.75 is below
+ * 448 / sqrt(2), so no rotation of the block saturates: K keeps its scale at
+ * every position, and raw K shares it.  Where the scale grows, the codes of the
+ * rows before the first written one follow by the power of two (exact, but for
+ * entries that become subnormal, which round to nearest even).  Entries that
+ * are not finite do not set the scale: infinities saturate, NaN stays.
+ * Each page written belongs to one sequence of the batch; a sequence with
+ * kv_len < q_len raises the device error flag and is skipped.
+ * Errors: KVM_ERR_INVALID_ARG, KVM_ERR_CAPACITY.
+ */
+kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cache,
+                         int32_t layer, const void *k, int64_t k_stride, const void *v,
+                         int64_t v_stride, const int32_t *positions, void *raw_k_pages,
+                         kvm_stream stream);
+
+/*
+ * Attention of a batch's newest tokens over one layer of the paged cache.  For
+ * query head h (kv head g = h / (H/G)) of token i of a sequence:
+ *   w_j = exp(softmax_scale * q . k_j) over the keys j < kv_len, with causal
+ *         also j <= kv_len - q_len + i
+ *   out = sum_j w_j v_j / sum_j w_j,   lse = log(sum_j w_j)
+ * A row that sees no key gets out = 0 and lse = -infinity.  One call serves a
+ * decoded token, the queries of an agent step, and a chunk of prefill whose own
+ * K / V were appended before.
+ * q     device, q_dtype: token row i at q + i * q_stride elements, H heads of d
+ *       (rotated; kvm_qk_norm_rope's q_rot).
+ * out   device, q_dtype, token row i at out + i * out_stride elements.
+ * lse   nullable, device float32 [n_tokens][H].
+ * Bases and strides multiples of 16 bytes; all buffers device memory.
+ * softmax_scale is usually 1 / sqrt(d); finite.
+ * bf16 queries over bf16 or e4m3 pages run on the tensor cores: products and
+ * sums in float32, with the weights rounded to 16 bits before the product
+ * with V.  Every other pairing of types runs in float32 throughout.
+ * Cache rows at or behind kv_len are not read into the result whatever they
+ * hold.  Rows below kv_len that causality hides from some queries of the batch
+ * are read for the others and must hold finite values.
+ * The call uses the context's workspace.
+ * Errors: KVM_ERR_INVALID_ARG, KVM_ERR_CAPACITY.
+ */
+kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cache,
+                      int32_t layer, const void *q, int64_t q_stride, float softmax_scale,
+                      int32_t causal, void *out, int64_t out_stride, float *lse,
+                      kvm_stream stream);
+
+/*
+ * kvm_build_index for e4m3 K pages with scales: index = k_scale * mean of the
+ * un-rotated codes (rounded once), and raw_k_out (nullable) takes the un-rotated
+ * codes, which keep the pages' scales.
+ * k_scale  device [n_blocks][L][G] float32: row i belongs to k_pages block i.
+ * Everything else, errors included, as kvm_build_index; KVM_ERR_INVALID_ARG
+ * unless kv_dtype is KVM_E4M3.
+ */
+kvm_status kvm_build_index_scaled(kvm_ctx *ctx, const void *k_pages, const float *k_scale,
+                                  int64_t first_block, int64_t n_blocks, void *index,
+                                  void *raw_k_out, kvm_stream stream);
+
 /* Wait for all work of the context (its internal streams and `stream`) and
  * report a raised device error flag (KVM_ERR_DEVICE), clearing it. */
 kvm_status kvm_sync(kvm_ctx *ctx, kvm_stream stream);

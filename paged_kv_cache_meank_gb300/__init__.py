@@ -8,6 +8,9 @@ the library's CUDA kernels.  The names follow the C ABI:
   Context.score_select   kvm_score_select   Eq. (10) scoring + budgeted top-k
   Context.assemble_view  kvm_assemble_view  gather + re-RoPE + V copy
   Context.step           kvm_step           one working-set update with page reuse
+  Context.qk_norm_rope   kvm_qk_norm_rope   per-head norm of q and k + rotation
+  Context.append_kv      kvm_append_kv      new K / V into a paged cache, K rotated
+  Context.attend         kvm_attend         attention over the paged cache
 
 Sources: "KVMem: Virtualizing Million-Token Agent Workspaces on a Consumer GPU"
 (§4.3, §4.4, §5) and "InferScale: GPU-Native KV Injection for Personalized LLM
@@ -21,11 +24,12 @@ from collections.abc import Mapping
 import torch
 
 from . import _abi
-from ._abi import (KVM_BF16, KVM_DEVICE, KVM_E4M3, KVM_F32, KVM_HOST_PINNED, KvmBuffers,
-                   KvmConfig, KvmError, KvmStepStats, KvmTierStats, check, load)
+from ._abi import (KVM_BF16, KVM_DEVICE, KVM_E4M3, KVM_F32, KVM_HOST_PINNED, KvmBatch,
+                   KvmBuffers, KvmCache, KvmConfig, KvmError, KvmStepStats, KvmTierStats, check,
+                   load)
 from .configs import BLOCK_TOKENS, Workload
 
-__all__ = ["Context", "HostTier", "KvmError", "config_for", "launch_count", "load", "KVM_F32",
+__all__ = ["Batch", "Cache", "Context", "HostTier", "KvmError", "config_for", "launch_count", "load", "KVM_F32",
            "KVM_BF16", "KVM_E4M3", "KVM_DEVICE", "KVM_HOST_PINNED"]
 
 _DT = {"f32": KVM_F32, "bf16": KVM_BF16, "e4m3": KVM_E4M3}
@@ -174,6 +178,33 @@ class StepStats(Mapping):
         return len(self._KEYS)
 
 
+class Cache:
+    """A kvm_cache: one paged cache's tensors (kept alive here), from Context.cache()."""
+
+    def __init__(self, k_pages, v_pages, k_scale, v_scale):
+        self.tensors = (k_pages, v_pages, k_scale, v_scale)
+        self.c = KvmCache(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                          k_pages.shape[0], 0 if k_scale is None else k_scale.shape[0])
+        self.ref = ctypes.addressof(self.c)
+
+
+class Batch:
+    """A kvm_batch: a batch's lengths and page tables (kept alive here), from
+    Context.batch()."""
+
+    def __init__(self, q_start, kv_len, page_table, scale_rows, n_tokens, max_q_len, max_kv_len):
+        self.tensors = (q_start, kv_len, page_table, scale_rows)
+        self.n_tokens = n_tokens
+        self.c = KvmBatch(kv_len.shape[0], n_tokens, max_q_len, max_kv_len, _ptr(q_start),
+                          _ptr(kv_len), _ptr(page_table), _ptr(scale_rows), page_table.shape[1])
+        self.ref = ctypes.addressof(self.c)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
 class Context:
     """A kvm_ctx plus its caller-owned device workspace (a torch uint8 tensor)."""
 
@@ -210,7 +241,18 @@ class Context:
 
     # -- the four calls -----------------------------------------------------
     def build_index(self, k_pages, first_block: int, n_blocks: int, index, raw_k_out=None,
-                    stream=None) -> None:
+                    stream=None, k_scale=None) -> None:
+        """kvm_build_index; with ``k_scale`` ([n_blocks][L][G] float32, e4m3
+        pages) kvm_build_index_scaled."""
+        if k_scale is not None:
+            c = self.cfg
+            _need(k_scale.dtype == torch.float32 and k_scale.is_contiguous()
+                  and k_scale.shape[1:] == (c.n_layers, c.n_kv_heads)
+                  and k_scale.shape[0] >= n_blocks, "k_scale: float32 [n_blocks][L][G]")
+            check(self.lib.kvm_build_index_scaled(
+                self.handle, _ptr(k_pages), _ptr(k_scale), first_block, n_blocks, _ptr(index),
+                _ptr(raw_k_out), _stream(stream)), "kvm_build_index_scaled")
+            return
         check(self.lib.kvm_build_index(self.handle, _ptr(k_pages), first_block, n_blocks,
                                        _ptr(index), _ptr(raw_k_out), _stream(stream)),
               "kvm_build_index")
@@ -240,6 +282,105 @@ class Context:
         self._bound = dict(index=index, raw_k=raw_k, v=v, pool_k=pool_k, pool_v=pool_v,
                            pool_raw_k=pool_raw_k, page_table=page_table, scores=scores,
                            sel_ids=sel_ids)
+
+    # -- around the recall: one layer's attention ---------------------------
+    def cache(self, k_pages, v_pages, k_scale=None, v_scale=None) -> Cache:
+        """A paged cache: K / V pages [n_pages][L][G][32][d] of the context's
+        kv_dtype (e4m3 as uint8) and, for e4m3, scales [rows][L][G] float32."""
+        c = self.cfg
+        page = (c.n_layers, c.n_kv_heads, BLOCK_TOKENS, c.head_dim)
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            _need(t.dtype == self.kv_dtype and t.is_contiguous() and tuple(t.shape[1:]) == page,
+                  f"{name}: contiguous {self.kv_dtype} [n_pages][L][G][32][d]")
+        _need(k_pages.shape[0] == v_pages.shape[0], "as many K pages as V pages")
+        _need((k_scale is None) == (v_scale is None), "both scales or none")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _need(t is None or (t.dtype == torch.float32 and t.is_contiguous()
+                                and tuple(t.shape[1:]) == page[:2]
+                                and t.shape == k_scale.shape),
+                  f"{name}: contiguous float32 [rows][L][G]")
+        return Cache(k_pages, v_pages, k_scale, v_scale)
+
+    def batch(self, q_start, kv_len, page_table, *, n_tokens: int, max_q_len: int,
+              max_kv_len: int, scale_rows=None) -> Batch:
+        """A batch of sequences: int32 device tensors q_start [n + 1], kv_len [n],
+        page_table [n][pages] and optionally scale_rows, as page_table.  Its
+        bounds are host numbers; the tensors are read when kernels run."""
+        n = kv_len.shape[0]
+        for name, t, shape in (("q_start", q_start, (n + 1,)), ("kv_len", kv_len, (n,)),
+                               ("page_table", page_table, (n,) + tuple(page_table.shape[1:])),
+                               ("scale_rows", scale_rows, tuple(page_table.shape))):
+            _need(t is None or (t.dtype == torch.int32 and t.is_contiguous()
+                                and tuple(t.shape) == shape), f"{name}: contiguous int32 {shape}")
+        _need(page_table.dim() == 2, "page_table: [n_seqs][pages]")
+        return Batch(q_start, kv_len, page_table, scale_rows, n_tokens, max_q_len, max_kv_len)
+
+    def _rows(self, name, t, heads: int, n: int) -> int:
+        """Checks token rows [n][heads][d] of q_dtype; returns their stride."""
+        d = self.cfg.head_dim
+        _need(t.dtype == _TDT[self.cfg.q_dtype] and t.dim() == 3 and t.shape[0] >= n
+              and t.shape[1] == heads and t.shape[2] == d and t.stride(2) == 1
+              and t.stride(1) == d, f"{name}: [>= {n}][{heads}][{d}], heads packed")
+        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+
+    def qk_norm_rope(self, positions, q=None, k=None, *, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, q_free=None, q_rot=None, k_free=None, k_rot=None,
+                     stream=None) -> None:
+        """kvm_qk_norm_rope: q [n][H][d] and k [n][G][d] (any row stride)
+        normalised per head (where a weight [d] is given) and rotated at
+        ``positions`` (int32 [n]); the packed outputs given are written."""
+        c, dt = self.cfg, _TDT[self.cfg.q_dtype]
+        n = positions.shape[0]
+        _need(positions.dtype == torch.int32 and positions.is_contiguous(),
+              "positions: contiguous int32")
+        strides = [0, 0]
+        for i, (x, w, heads, outs) in enumerate(((q, q_weight, c.n_q_heads, (q_free, q_rot)),
+                                                 (k, k_weight, c.n_kv_heads, (k_free, k_rot)))):
+            side = "qk"[i]
+            if x is not None:
+                strides[i] = self._rows(side, x, heads, n)
+            _need(w is None or (w.dtype == dt and w.is_contiguous() and w.numel() == c.head_dim),
+                  f"{side}_weight: {dt} [d]")
+            for o in outs:
+                _need(o is None or (o.dtype == dt and o.is_contiguous()
+                                    and o.numel() >= n * heads * c.head_dim),
+                      f"{side} outputs: contiguous {dt} [n][heads][d]")
+        check(self.lib.kvm_qk_norm_rope(
+            self.handle, n, _ptr(positions), _ptr(q), strides[0], _ptr(k), strides[1],
+            _ptr(q_weight), _ptr(k_weight), eps, _ptr(q_free), _ptr(q_rot), _ptr(k_free),
+            _ptr(k_rot), _stream(stream)), "kvm_qk_norm_rope")
+
+    def append_kv(self, batch: Batch, cache: Cache, layer: int, k, v, *, positions=None,
+                  raw_k_pages=None, stream=None) -> None:
+        """kvm_append_kv: the batch's newest tokens (RoPE-free k and v, [n][G][d],
+        any row stride) into ``layer`` of the cache, K rotated at ``positions``
+        (int32 [n]; default: the logical index)."""
+        n, G = batch.n_tokens, self.cfg.n_kv_heads
+        ks, vs = self._rows("k", k, G, n), self._rows("v", v, G, n)
+        _need(positions is None or (positions.dtype == torch.int32 and positions.is_contiguous()
+                                    and positions.numel() >= n), "positions: int32 [n]")
+        _need(raw_k_pages is None or (raw_k_pages.dtype == self.kv_dtype
+                                      and raw_k_pages.is_contiguous()
+                                      and raw_k_pages.shape == cache.tensors[0].shape),
+              "raw_k_pages: as k_pages")
+        check(self.lib.kvm_append_kv(self.handle, batch.ref, cache.ref, layer, _ptr(k), ks,
+                                     _ptr(v), vs, _ptr(positions), _ptr(raw_k_pages),
+                                     _stream(stream)), "kvm_append_kv")
+
+    def attend(self, batch: Batch, cache: Cache, layer: int, q, out, *, lse=None,
+               scale: float | None = None, causal: bool = True, stream=None) -> None:
+        """kvm_attend: attention of the batch's newest tokens (q [n][H][d],
+        rotated; any row stride) over ``layer`` of the cache into ``out``; lse
+        float32 [n][H].  scale defaults to 1 / sqrt(d)."""
+        c, n = self.cfg, batch.n_tokens
+        qs, outs = self._rows("q", q, c.n_q_heads, n), self._rows("out", out, c.n_q_heads, n)
+        _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous()
+                              and lse.numel() >= n * c.n_q_heads), "lse: float32 [n][H]")
+        if scale is None:
+            scale = c.head_dim ** -0.5
+        check(self.lib.kvm_attend(self.handle, batch.ref, cache.ref, layer, _ptr(q), qs, scale,
+                                  1 if causal else 0, _ptr(out), outs, _ptr(lse),
+                                  _stream(stream)), "kvm_attend")
 
     def stage_out(self, raw_k, v, first_block: int, n_blocks: int, stream=None) -> None:
         """kvm_stage_out: copy completed blocks' raw K / V into the bound host

@@ -62,6 +62,24 @@ class KvmTierStats(ctypes.Structure):
     ]
 
 
+class KvmCache(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64), ("n_scale_rows", ctypes.c_int64),
+    ]
+
+
+class KvmBatch(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+        ("max_q_len", ctypes.c_int32), ("max_kv_len", ctypes.c_int32),
+        ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("scale_rows", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "kvm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvmConfig)]),
@@ -96,6 +114,22 @@ SIGNATURES = {
                                      ctypes.POINTER(KvmTierStats)]),
     "kvm_tier_resident": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64]),
     "kvm_tier_destroy": (ctypes.c_int, [ctypes.c_void_p]),
+    "kvm_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvm_append_kv": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p]),
+    "kvm_attend": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                  ctypes.c_float, ctypes.c_int32, ctypes.c_void_p,
+                                  ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "kvm_build_index_scaled": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p]),
     "kvm_sync": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
     "kvm_graph_step_stats": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "kvm_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -23,6 +23,7 @@ LIB = os.path.join(PKG, "libkvm.so")
 SOURCES = [
     "rope_table.cu",
     "meank.cu",
+    "meank_scaled.cu",
     "score.cu",
     "score_tc.cu",
     "score_tc1.cu",
@@ -31,8 +32,12 @@ SOURCES = [
     "select.cu",
     "assemble.cu",
     "residency.cu",
+    "norm_rope.cu",
+    "append.cu",
+    "attend.cu",
     "score_static.cu",
     "kvm_api.cpp",
+    "serve_api.cpp",
     "host_tier.cpp",
 ]
 

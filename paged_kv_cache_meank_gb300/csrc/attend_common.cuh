@@ -1,0 +1,163 @@
+// Work split of the paged attention kernels, shared by all of them.
+//
+// The work of a call is a line of units: for each sequence, each kv head, each
+// tile of RB query rows (row = token * (H/G) + head in the group), one unit per
+// `unit` keys that the tile sees (one unit for a tile that sees none, which
+// still writes its rows).  The lengths live in device memory, so every CTA
+// lays the line out itself, one prefix sum over the sequences, and takes an
+// equal run of it: a ragged batch balances without the host knowing a length.  A
+// run cuts a tile's keys at its two ends only.  A tile whole within one CTA is
+// written at once; the CTAs that share one each leave an unnormalised sum with
+// its running maximum and weight, and they are joined in CTA order, so that
+// results do not depend on which CTA came last.
+#pragma once
+
+#include "kvm_internal.cuh"
+
+namespace kvm {
+
+struct SeqInfo {
+    int q0, q_len, kv;
+};
+
+// The lengths of a sequence; q_len = 0 and *ok = false where they are out of
+// their bounds.
+__host__ __device__ __forceinline__ SeqInfo seq_info(const BatchArgs &b, int s, bool *ok) {
+    SeqInfo i;
+    i.q0 = b.q_start[s];
+    const int q1 = b.q_start[s + 1];
+    i.kv = b.kv_len[s];
+    *ok = i.q0 >= 0 && q1 >= i.q0 && q1 <= b.n_tokens && q1 - i.q0 <= b.max_q_len && i.kv >= 0 &&
+          i.kv <= b.max_kv_len;
+    i.q_len = *ok ? q1 - i.q0 : 0;
+    return i;
+}
+
+template <int RB, int UNIT>
+struct Line {
+    // Keys that row tile r of a sequence sees (its last row sees the most).
+    __host__ __device__ static __forceinline__ int keys(const SeqInfo &i, int gqa, int causal, int r) {
+        if (!causal) return i.kv;
+        const int row_end = min(i.q_len * gqa, (r + 1) * RB);
+        return max(0, min(i.kv, i.kv - i.q_len + (row_end - 1) / gqa + 1));
+    }
+    __host__ __device__ static __forceinline__ int tiles(const SeqInfo &i, int gqa) {
+        return (i.q_len * gqa + RB - 1) / RB;
+    }
+    __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, int gqa, int causal, int r) {
+        return max(1, (keys(i, gqa, causal, r) + UNIT - 1) / UNIT);
+    }
+    // pre[s] = units of the sequences before s (pre: kMaxSeqs + 1 in shared
+    // memory).  Called by the whole CTA; ends with a barrier.
+    __device__ static void lay_out(const AttendArgs &a, int64_t *pre) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+        for (int s = warp; s < a.b.n_seqs; s += warps) {
+            bool ok;
+            const SeqInfo i = seq_info(a.b, s, &ok);
+            if (!ok && lane == 0) atomicOr(a.b.err, kErrBatch);
+            int64_t w = 0;
+            const int n = tiles(i, a.gqa);
+            for (int r = lane; r < n; r += 32) w += weight(i, a.gqa, a.causal, r);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            if (lane == 0) pre[s + 1] = w * a.b.G;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int64_t run = 0;
+            for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
+                const int s = s0 + lane;
+                int64_t w = s < a.b.n_seqs ? pre[s + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
+                    if (lane >= o) w += up;
+                }
+                if (s < a.b.n_seqs) pre[s + 1] = run + w;
+                run += __shfl_sync(0xffffffffu, w, 31);
+            }
+            if (lane == 0) pre[0] = 0;
+        }
+        __syncthreads();
+    }
+};
+
+// A walk over one CTA's run of the line.
+template <int RB, int UNIT>
+struct Walk {
+    using LN = Line<RB, UNIT>;
+    int64_t x, end, per;     // position, end of the run, units of a run
+    int s, g, r, n_tiles;    // sequence, kv head, row tile
+    int u0, u1, w;           // the segment's units [u0, u1) of the tile's w
+    int nk;                  // keys the tile sees
+    SeqInfo i;
+
+    // per: units of one CTA's run.  False when the run is empty.
+    __host__ __device__ __forceinline__ bool start(const AttendArgs &a, const int64_t *pre, int cta,
+                                          int n_ctas, int min_units) {
+        const int64_t total = pre[a.b.n_seqs];
+        per = max((int64_t)min_units, (total + n_ctas - 1) / n_ctas);
+        x = cta * per;
+        end = min(total, x + per);
+        if (x >= end) return false;
+        int lo = 0, hi = a.b.n_seqs - 1;                // the last s with pre[s] <= x
+        while (lo < hi) {
+            const int m = (lo + hi + 1) >> 1;
+            if (pre[m] <= x) lo = m; else hi = m - 1;
+        }
+        s = lo;
+        bool ok;
+        i = seq_info(a.b, s, &ok);
+        n_tiles = LN::tiles(i, a.gqa);
+        int64_t rem = x - pre[s];
+        const int64_t per_head = (pre[s + 1] - pre[s]) / a.b.G;
+        g = (int)(rem / per_head);
+        rem -= g * per_head;
+        r = 0;
+        for (w = LN::weight(i, a.gqa, a.causal, 0); rem >= w; w = LN::weight(i, a.gqa, a.causal, r)) {
+            rem -= w;
+            ++r;
+        }
+        u0 = (int)rem;
+        fill(a);
+        return true;
+    }
+    __host__ __device__ __forceinline__ void fill(const AttendArgs &a) {
+        nk = LN::keys(i, a.gqa, a.causal, r);
+        u1 = (int)min((int64_t)w, u0 + (end - x));
+    }
+    __host__ __device__ __forceinline__ bool next(const AttendArgs &a, const int64_t *pre) {
+        x += u1 - u0;
+        if (x >= end) return false;
+        u0 = 0;
+        if (++r == n_tiles) {
+            r = 0;
+            if (++g == a.b.G) {
+                g = 0;
+                do ++s; while (pre[s + 1] <= x);        // skips sequences without rows
+                bool ok;
+                i = seq_info(a.b, s, &ok);
+                n_tiles = LN::tiles(i, a.gqa);
+            }
+        }
+        w = LN::weight(i, a.gqa, a.causal, r);
+        fill(a);
+        return true;
+    }
+    __host__ __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == w; }
+    // The first and last CTA that share the segment's tile.
+    __host__ __device__ __forceinline__ int first_cta() const { return (int)((x - u0) / per); }
+    __host__ __device__ __forceinline__ int last_cta() const { return (int)((x - u0 + w - 1) / per); }
+};
+
+// A CTA's two places for partial results: 1 for a tile that goes on in the next
+// CTA and begins in this one, 0 for a tile that began in an earlier one.
+__host__ __device__ __forceinline__ size_t part_slot(int cta, bool first) {
+    return (size_t)cta * 2 + (first ? 1 : 0);
+}
+
+constexpr size_t kAttendPartFloats = (size_t)160 * 2 * 256 * 130;
+
+cudaError_t launch_attend_simt(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s);
+
+}  // namespace kvm

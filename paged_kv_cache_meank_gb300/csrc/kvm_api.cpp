@@ -54,7 +54,7 @@ constexpr int kStatSlots = 64;   // steps whose counters can wait for kvm_sync
 
 struct Layout {
     size_t table, part_m, part_z, row_m, row_invz, partial, fused, qstage, stage0, stage1, keep,
-        desc, sel, resid, err, total;
+        desc, sel, resid, attend, attend_count, err, total;
     size_t qstage_bytes;
     size_t stage_bytes;
     int64_t keep_tiles;   // index tiles pass 1 keeps in device memory for pass 2
@@ -158,6 +158,8 @@ Layout layout_of(const kvm_config *c) {
     lo.resid = take(((size_t)2 * c->max_blocks + (size_t)4 * c->pool_pages + c->view_blocks +
                      (size_t)(kStatSlots + 1) * 8 + 1) *
                     sizeof(int32_t));
+    lo.attend = take(kvm::attend_scratch_bytes());
+    lo.attend_count = take(kvm::kAttendMaxCtas * sizeof(int));
     lo.err = take(256);
     lo.total = off;
     return lo;
@@ -342,6 +344,25 @@ static kvm_status kernel_ptr(T *p, T **out, const char *what) {
     return st;
 }
 
+kvm::CtxView kvm::ctx_view(const kvm_ctx *c) {
+    CtxView v{};
+    v.L = c->cfg.n_layers;
+    v.G = c->cfg.n_kv_heads;
+    v.H = c->cfg.n_q_heads;
+    v.d = c->cfg.head_dim;
+    v.kv_dtype = c->cfg.kv_dtype;
+    v.index_dtype = c->cfg.index_dtype;
+    v.q_dtype = c->cfg.q_dtype;
+    v.max_blocks = c->cfg.max_blocks;
+    v.max_positions = c->cfg.max_positions;
+    v.table = c->table;
+    v.err = c->err_dev;
+    v.attend_part = reinterpret_cast<float *>(c->ws + c->lo.attend);
+    v.attend_count = reinterpret_cast<int *>(c->ws + c->lo.attend_count);
+    v.device = c->device;
+    return v;
+}
+
 extern "C" {
 
 size_t kvm_workspace_bytes(const kvm_config *cfg) {
@@ -438,7 +459,9 @@ kvm_status kvm_create(const kvm_config *cfg, void *workspace, size_t workspace_b
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if ((e = kvm::launch_rope_table(c->table, cfg->max_positions, hd, om, s)) != cudaSuccess)
         return cleanup(cuda_fail(e, "rope table"));
-    if ((e = cudaMemsetAsync(c->err_dev, 0, sizeof(int), s)) != cudaSuccess)
+    if ((e = cudaMemsetAsync(c->err_dev, 0, sizeof(int), s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(c->ws + lo.attend_count, 0, kvm::kAttendMaxCtas * sizeof(int), s)) !=
+            cudaSuccess)
         return cleanup(cuda_fail(e, "cudaMemsetAsync"));
     if (c->device_diff) {
         // an empty pool; no block has been selected yet (stamp 0 < every epoch)

@@ -8,6 +8,8 @@
 
 #include <string>
 
+struct kvm_ctx;
+
 namespace kvm {
 
 // Sets the message kvm_last_error() returns on the calling thread.
@@ -22,6 +24,18 @@ void note_launch();
 // kvm_status value (KVM_OK, KVM_ERR_INVALID_ARG or KVM_ERR_CUDA) and sets the
 // last-error message.  Defined in kvm_api.cpp.
 int resolve_kernel_ptr(const void *p, const void **out, const char *what);
+
+// What the entry points outside kvm_api.cpp need of a context.
+struct CtxView {
+    int L, G, H, d, kv_dtype, index_dtype, q_dtype;
+    int64_t max_blocks, max_positions;
+    const float2 *table;   // cos/sin, [max_positions][d / 2]
+    int *err;              // device error flag
+    float *attend_part;    // kvm_attend: partial outputs of split rows
+    int *attend_count;     // kvm_attend: arrivals per CTA, zero between calls
+    int device;
+};
+CtxView ctx_view(const kvm_ctx *c);
 
 constexpr int kBlockTokens = 32;
 constexpr int kMaxHalfDim = 64;       // head_dim <= 128
@@ -70,6 +84,12 @@ cudaError_t launch_meank(int kv_dtype, int index_dtype, int d, const void *k_pag
                          void *raw_out, void *index, int64_t index_cap, int64_t first_block,
                          int64_t n_blocks, int LG, const float2 *table, int *err,
                          cudaStream_t s);
+
+// ---- meank_scaled.cu
+cudaError_t launch_meank_scaled(int index_dtype, int d, const void *k_pages, const float *k_scale,
+                                void *raw_out, void *index, int64_t index_cap,
+                                int64_t first_block, int64_t n_blocks, int LG,
+                                const float2 *table, int *err, cudaStream_t s);
 
 // ---- assemble.cu
 // Slots given by (sel_ids, page_ids) against repository / page base pointers.
@@ -191,6 +211,66 @@ size_t select_scratch_bytes();
 // memory of select_scratch_bytes(), used by long histories only.
 cudaError_t launch_select(const float *scores, int64_t n_blocks, int sink, int recent,
                           int view_blocks, int32_t *sel_ids, int *scratch, cudaStream_t s);
+
+// ---- norm_rope.cu
+struct NormArgs {
+    int n_tokens, H, G, d;
+    const int32_t *positions;
+    const void *q, *k;             // either may be NULL
+    int64_t q_stride, k_stride;    // elements
+    const void *q_weight, *k_weight;
+    float eps;
+    void *q_free, *q_rot, *k_free, *k_rot;
+    const float2 *table;
+    int64_t max_positions;
+    int *err;
+};
+cudaError_t launch_norm_rope(int dtype, const NormArgs &a, cudaStream_t s);
+
+// ---- append.cu, attend*.cu: a batch over one layer of a paged cache
+struct BatchArgs {
+    int n_seqs, n_tokens, max_q_len, max_kv_len;
+    const int32_t *q_start, *kv_len, *page_table, *scale_rows;
+    int64_t table_stride, n_pages, n_scale_rows;
+    int L, G, layer;
+    int *err;
+};
+// Raised in the device error word by the batch kernels.
+constexpr int kErrBatch = 8;       // a length, page, scale row or position out of range
+constexpr int kErrScale = 16;      // a scale that is not a power of two in range
+
+constexpr int kMaxSeqs = 1024;
+
+struct AppendArgs {
+    BatchArgs b;
+    const void *k, *v;             // new rows, elements of q_dtype
+    int64_t k_stride, v_stride;
+    const int32_t *positions;      // NULL: the logical index
+    void *k_pages, *v_pages, *raw_pages;
+    float *k_scale, *v_scale;      // NULL: unit scale
+    const float2 *table;
+    int64_t max_positions;
+};
+cudaError_t launch_append(int q_dtype, int kv_dtype, int d, const AppendArgs &a, cudaStream_t s);
+
+struct AttendArgs {
+    BatchArgs b;
+    int H, gqa, d;
+    const void *q;
+    int64_t q_stride;
+    const void *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    float scale;                   // softmax scale
+    int causal;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    float *part;                   // partial outputs (attend_scratch_bytes)
+    int *count;                    // arrivals, [kAttendMaxCtas]
+};
+constexpr int kAttendMaxCtas = 608;    // CTAs of one attention grid, at most
+size_t attend_scratch_bytes();         // of AttendArgs::part
+cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s);
 
 // Multiprocessors of the current device (152 where it cannot be read).
 int sm_count();

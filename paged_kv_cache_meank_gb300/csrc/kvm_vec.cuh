@@ -124,4 +124,34 @@ __device__ inline float to_float<__nv_bfloat16>(__nv_bfloat16 x) {
     return __bfloat162float(x);
 }
 
+// N float32 values stored as T at p (aligned to min(16, N * sizeof(T)) bytes).
+template <typename T, int N>
+__device__ inline void store_n(T *p, const float (&f)[N]) {
+    using VT = VecTraits<T>;
+    if constexpr (N == VT::N) {
+        *reinterpret_cast<typename VT::V *>(p) = VT::pack(f);
+    } else if constexpr (N > VT::N) {      // 8 values as float32: two vectors
+        float lo[VT::N], hi[VT::N];
+#pragma unroll
+        for (int i = 0; i < VT::N; ++i) {
+            lo[i] = f[i];
+            hi[i] = f[VT::N + i];
+        }
+        reinterpret_cast<typename VT::V *>(p)[0] = VT::pack(lo);
+        reinterpret_cast<typename VT::V *>(p)[1] = VT::pack(hi);
+    } else if constexpr (sizeof(T) == 2) { // 4 values as bf16
+        *reinterpret_cast<uint2 *>(p) = make_uint2(VT::pack2(f[0], f[1]), VT::pack2(f[2], f[3]));
+    } else {                               // 4 values as e4m3
+        *reinterpret_cast<uint32_t *>(p) = VT::pack2(f[0], f[1]) | (VT::pack2(f[2], f[3]) << 16);
+    }
+}
+
+// A block's scale as read: a power of two 2^e with -100 <= e <= 119, or the
+// device error flag (bit 16) is raised.
+__device__ inline float checked_scale(float s, int *err) {
+    const uint32_t u = __float_as_uint(s);
+    if ((u & 0x807FFFFFu) != 0 || (u >> 23) - 27u > 219u) atomicOr(err, 16);
+    return s;
+}
+
 }  // namespace kvm
