@@ -97,9 +97,18 @@ struct Walk {
                                           int n_ctas, int min_units) {
         const int64_t total = pre[a.b.n_seqs];
         per = max((int64_t)min_units, (total + n_ctas - 1) / n_ctas);
-        x = cta * per;
+        if (cta * per >= total) return false;
+        start_at(a, pre, cta * per, per);
         end = min(total, x + per);
-        if (x >= end) return false;
+        fill(a);
+        return true;
+    }
+    // The position of one unit of the line; the run ends with that unit.
+    __host__ __device__ __forceinline__ void start_at(const AttendArgs &a, const int64_t *pre,
+                                                      int64_t at, int64_t per_) {
+        x = at;
+        per = per_;
+        end = at + 1;
         int lo = 0, hi = a.b.n_seqs - 1;                // the last s with pre[s] <= x
         while (lo < hi) {
             const int m = (lo + hi + 1) >> 1;
@@ -120,13 +129,12 @@ struct Walk {
         }
         u0 = (int)rem;
         fill(a);
-        return true;
     }
     __host__ __device__ __forceinline__ void fill(const AttendArgs &a) {
         nk = LN::keys(i, a.gqa, a.causal, r);
         u1 = (int)min((int64_t)w, u0 + (end - x));
     }
-    __host__ __device__ __forceinline__ bool next(const AttendArgs &a, const int64_t *pre) {
+    __host__ __device__ __forceinline__ bool next(const AttendArgs &a) {
         x += u1 - u0;
         if (x >= end) return false;
         u0 = 0;
@@ -134,10 +142,11 @@ struct Walk {
             r = 0;
             if (++g == a.b.G) {
                 g = 0;
-                do ++s; while (pre[s + 1] <= x);        // skips sequences without rows
-                bool ok;
-                i = seq_info(a.b, s, &ok);
-                n_tiles = LN::tiles(i, a.gqa);
+                do {                                    // skips sequences without rows
+                    bool ok;
+                    i = seq_info(a.b, ++s, &ok);
+                    n_tiles = LN::tiles(i, a.gqa);
+                } while (n_tiles == 0);
             }
         }
         w = LN::weight(i, a.gqa, a.causal, r);
@@ -156,8 +165,13 @@ __host__ __device__ __forceinline__ size_t part_slot(int cta, bool first) {
     return (size_t)cta * 2 + (first ? 1 : 0);
 }
 
-constexpr size_t kAttendPartFloats = (size_t)160 * 2 * 256 * 130;
+// CTAs and query rows of the largest records (the tensor-core tile kernel's).
+constexpr int kTileMaxCtas = 160, kTileMaxRows = 256;
+constexpr size_t kAttendPartFloats = (size_t)kTileMaxCtas * 2 * kTileMaxRows * 130;
 
-cudaError_t launch_attend_simt(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s);
+// attend_tc.cu: tensor-core tiles of 128 query rows, for bf16 queries over bf16
+// or e4m3 pages.
+bool attend_tc_supported(int q_dtype, int kv_dtype, const AttendArgs &a);
+cudaError_t launch_attend_tc(int kv_dtype, const AttendArgs &a, cudaStream_t s);
 
 }  // namespace kvm
