@@ -83,7 +83,8 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -200,11 +201,6 @@ class Batch:
         self.ref = ctypes.addressof(self.c)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
-
-
 class Context:
     """A kvm_ctx plus its caller-owned device workspace (a torch uint8 tensor)."""
 
@@ -221,6 +217,8 @@ class Context:
         self.handle = h
         self._bound = None
         self._pending = []
+        # read on every call: plain attributes are cheaper than ctypes fields
+        self._shape = (cfg.n_q_heads, cfg.n_kv_heads, cfg.head_dim, _TDT[cfg.q_dtype])
 
     # -- shapes -----------------------------------------------------------
     @property
@@ -246,9 +244,10 @@ class Context:
         pages) kvm_build_index_scaled."""
         if k_scale is not None:
             c = self.cfg
-            _need(k_scale.dtype == torch.float32 and k_scale.is_contiguous()
-                  and k_scale.shape[1:] == (c.n_layers, c.n_kv_heads)
-                  and k_scale.shape[0] >= n_blocks, "k_scale: float32 [n_blocks][L][G]")
+            if not (k_scale.dtype is torch.float32 and k_scale.is_contiguous()
+                    and k_scale.shape[1:] == (c.n_layers, c.n_kv_heads)
+                    and k_scale.shape[0] >= n_blocks):
+                raise ValueError("k_scale: contiguous float32 [n_blocks][L][G]")
             check(self.lib.kvm_build_index_scaled(
                 self.handle, _ptr(k_pages), _ptr(k_scale), first_block, n_blocks, _ptr(index),
                 _ptr(raw_k_out), _stream(stream)), "kvm_build_index_scaled")
@@ -289,16 +288,16 @@ class Context:
         kv_dtype (e4m3 as uint8) and, for e4m3, scales [rows][L][G] float32."""
         c = self.cfg
         page = (c.n_layers, c.n_kv_heads, BLOCK_TOKENS, c.head_dim)
-        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-            _need(t.dtype == self.kv_dtype and t.is_contiguous() and tuple(t.shape[1:]) == page,
-                  f"{name}: contiguous {self.kv_dtype} [n_pages][L][G][32][d]")
-        _need(k_pages.shape[0] == v_pages.shape[0], "as many K pages as V pages")
-        _need((k_scale is None) == (v_scale is None), "both scales or none")
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _need(t is None or (t.dtype == torch.float32 and t.is_contiguous()
-                                and tuple(t.shape[1:]) == page[:2]
-                                and t.shape == k_scale.shape),
-                  f"{name}: contiguous float32 [rows][L][G]")
+        for t in (k_pages, v_pages):
+            if not (t.dtype is self.kv_dtype and t.is_contiguous() and t.shape[1:] == page
+                    and t.shape == k_pages.shape):
+                raise ValueError(f"pages: contiguous {self.kv_dtype} [n_pages][L][G][32][d]")
+        if (k_scale is None) != (v_scale is None):
+            raise ValueError("both scales or none")
+        for t in (k_scale, v_scale):
+            if t is not None and not (t.dtype is torch.float32 and t.is_contiguous()
+                                      and t.shape[1:] == page[:2] and t.shape == k_scale.shape):
+                raise ValueError("scales: contiguous float32 [rows][L][G]")
         return Cache(k_pages, v_pages, k_scale, v_scale)
 
     def batch(self, q_start, kv_len, page_table, *, n_tokens: int, max_q_len: int,
@@ -307,21 +306,33 @@ class Context:
         page_table [n][pages] and optionally scale_rows, as page_table.  Its
         bounds are host numbers; the tensors are read when kernels run."""
         n = kv_len.shape[0]
+        if page_table.dim() != 2:
+            raise ValueError("page_table: [n_seqs][pages]")
         for name, t, shape in (("q_start", q_start, (n + 1,)), ("kv_len", kv_len, (n,)),
-                               ("page_table", page_table, (n,) + tuple(page_table.shape[1:])),
-                               ("scale_rows", scale_rows, tuple(page_table.shape))):
-            _need(t is None or (t.dtype == torch.int32 and t.is_contiguous()
-                                and tuple(t.shape) == shape), f"{name}: contiguous int32 {shape}")
-        _need(page_table.dim() == 2, "page_table: [n_seqs][pages]")
+                               ("page_table", page_table, (n, page_table.shape[1])),
+                               ("scale_rows", scale_rows, page_table.shape)):
+            if t is not None and not (t.dtype is torch.int32 and t.is_contiguous()
+                                      and t.shape == shape):
+                raise ValueError(f"{name}: contiguous int32 {tuple(shape)}")
         return Batch(q_start, kv_len, page_table, scale_rows, n_tokens, max_q_len, max_kv_len)
 
     def _rows(self, name, t, heads: int, n: int) -> int:
         """Checks token rows [n][heads][d] of q_dtype; returns their stride."""
-        d = self.cfg.head_dim
-        _need(t.dtype == _TDT[self.cfg.q_dtype] and t.dim() == 3 and t.shape[0] >= n
-              and t.shape[1] == heads and t.shape[2] == d and t.stride(2) == 1
-              and t.stride(1) == d, f"{name}: [>= {n}][{heads}][{d}], heads packed")
-        return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * d)
+        _, _, d, dt = self._shape
+        shape, stride = t.shape, t.stride()
+        if not (t.dtype is dt and len(shape) == 3 and shape[0] >= n and shape[1] == heads
+                and shape[2] == d and stride[2] == 1 and (stride[1] == d or heads == 1)):
+            raise ValueError(f"{name}: {dt} [>= {n}][{heads}][{d}], heads packed")
+        return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+
+    def _packed(self, name, t, heads: int, n: int) -> int | None:
+        """Checks a contiguous output [n][heads][d] of q_dtype; its address."""
+        if t is None:
+            return None
+        _, _, d, dt = self._shape
+        if not (t.dtype is dt and t.is_contiguous() and t.numel() >= n * heads * d):
+            raise ValueError(f"{name}: contiguous {dt} [{n}][{heads}][{d}]")
+        return t.data_ptr()
 
     def qk_norm_rope(self, positions, q=None, k=None, *, q_weight=None, k_weight=None,
                      eps: float = 1e-6, q_free=None, q_rot=None, k_free=None, k_rot=None,
@@ -329,42 +340,35 @@ class Context:
         """kvm_qk_norm_rope: q [n][H][d] and k [n][G][d] (any row stride)
         normalised per head (where a weight [d] is given) and rotated at
         ``positions`` (int32 [n]); the packed outputs given are written."""
-        c, dt = self.cfg, _TDT[self.cfg.q_dtype]
+        H, G, _, _ = self._shape
         n = positions.shape[0]
-        _need(positions.dtype == torch.int32 and positions.is_contiguous(),
-              "positions: contiguous int32")
-        strides = [0, 0]
-        for i, (x, w, heads, outs) in enumerate(((q, q_weight, c.n_q_heads, (q_free, q_rot)),
-                                                 (k, k_weight, c.n_kv_heads, (k_free, k_rot)))):
-            side = "qk"[i]
-            if x is not None:
-                strides[i] = self._rows(side, x, heads, n)
-            _need(w is None or (w.dtype == dt and w.is_contiguous() and w.numel() == c.head_dim),
-                  f"{side}_weight: {dt} [d]")
-            for o in outs:
-                _need(o is None or (o.dtype == dt and o.is_contiguous()
-                                    and o.numel() >= n * heads * c.head_dim),
-                      f"{side} outputs: contiguous {dt} [n][heads][d]")
+        if not (positions.dtype is torch.int32 and positions.is_contiguous()):
+            raise ValueError("positions: contiguous int32 [n]")
         check(self.lib.kvm_qk_norm_rope(
-            self.handle, n, _ptr(positions), _ptr(q), strides[0], _ptr(k), strides[1],
-            _ptr(q_weight), _ptr(k_weight), eps, _ptr(q_free), _ptr(q_rot), _ptr(k_free),
-            _ptr(k_rot), _stream(stream)), "kvm_qk_norm_rope")
+            self.handle, n, positions.data_ptr(),
+            _ptr(q), 0 if q is None else self._rows("q", q, H, n),
+            _ptr(k), 0 if k is None else self._rows("k", k, G, n),
+            self._packed("q_weight", q_weight, 1, 1), self._packed("k_weight", k_weight, 1, 1), eps,
+            self._packed("q_free", q_free, H, n), self._packed("q_rot", q_rot, H, n),
+            self._packed("k_free", k_free, G, n), self._packed("k_rot", k_rot, G, n),
+            _stream(stream)), "kvm_qk_norm_rope")
 
     def append_kv(self, batch: Batch, cache: Cache, layer: int, k, v, *, positions=None,
                   raw_k_pages=None, stream=None) -> None:
         """kvm_append_kv: the batch's newest tokens (RoPE-free k and v, [n][G][d],
         any row stride) into ``layer`` of the cache, K rotated at ``positions``
         (int32 [n]; default: the logical index)."""
-        n, G = batch.n_tokens, self.cfg.n_kv_heads
+        n, G = batch.n_tokens, self._shape[1]
         ks, vs = self._rows("k", k, G, n), self._rows("v", v, G, n)
-        _need(positions is None or (positions.dtype == torch.int32 and positions.is_contiguous()
-                                    and positions.numel() >= n), "positions: int32 [n]")
-        _need(raw_k_pages is None or (raw_k_pages.dtype == self.kv_dtype
-                                      and raw_k_pages.is_contiguous()
-                                      and raw_k_pages.shape == cache.tensors[0].shape),
-              "raw_k_pages: as k_pages")
-        check(self.lib.kvm_append_kv(self.handle, batch.ref, cache.ref, layer, _ptr(k), ks,
-                                     _ptr(v), vs, _ptr(positions), _ptr(raw_k_pages),
+        if positions is not None and not (positions.dtype is torch.int32
+                                          and positions.is_contiguous() and positions.numel() >= n):
+            raise ValueError("positions: contiguous int32 [n]")
+        if raw_k_pages is not None and not (raw_k_pages.dtype is self.kv_dtype
+                                            and raw_k_pages.is_contiguous()
+                                            and raw_k_pages.shape == cache.tensors[0].shape):
+            raise ValueError("raw_k_pages: as k_pages")
+        check(self.lib.kvm_append_kv(self.handle, batch.ref, cache.ref, layer, k.data_ptr(), ks,
+                                     v.data_ptr(), vs, _ptr(positions), _ptr(raw_k_pages),
                                      _stream(stream)), "kvm_append_kv")
 
     def attend(self, batch: Batch, cache: Cache, layer: int, q, out, *, lse=None,
@@ -372,15 +376,15 @@ class Context:
         """kvm_attend: attention of the batch's newest tokens (q [n][H][d],
         rotated; any row stride) over ``layer`` of the cache into ``out``; lse
         float32 [n][H].  scale defaults to 1 / sqrt(d)."""
-        c, n = self.cfg, batch.n_tokens
-        qs, outs = self._rows("q", q, c.n_q_heads, n), self._rows("out", out, c.n_q_heads, n)
-        _need(lse is None or (lse.dtype == torch.float32 and lse.is_contiguous()
-                              and lse.numel() >= n * c.n_q_heads), "lse: float32 [n][H]")
-        if scale is None:
-            scale = c.head_dim ** -0.5
-        check(self.lib.kvm_attend(self.handle, batch.ref, cache.ref, layer, _ptr(q), qs, scale,
-                                  1 if causal else 0, _ptr(out), outs, _ptr(lse),
-                                  _stream(stream)), "kvm_attend")
+        H, _, d, _ = self._shape
+        n = batch.n_tokens
+        qs, outs = self._rows("q", q, H, n), self._rows("out", out, H, n)
+        if lse is not None and not (lse.dtype is torch.float32 and lse.is_contiguous()
+                                    and lse.numel() >= n * H):
+            raise ValueError("lse: contiguous float32 [n][H]")
+        check(self.lib.kvm_attend(self.handle, batch.ref, cache.ref, layer, q.data_ptr(), qs,
+                                  d ** -0.5 if scale is None else scale, 1 if causal else 0,
+                                  out.data_ptr(), outs, _ptr(lse), _stream(stream)), "kvm_attend")
 
     def stage_out(self, raw_k, v, first_block: int, n_blocks: int, stream=None) -> None:
         """kvm_stage_out: copy completed blocks' raw K / V into the bound host

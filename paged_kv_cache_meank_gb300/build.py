@@ -35,6 +35,7 @@ SOURCES = [
     "norm_rope.cu",
     "append.cu",
     "attend.cu",
+    "attend_decode.cu",
     "attend_tc.cu",
     "score_static.cu",
     "kvm_api.cpp",

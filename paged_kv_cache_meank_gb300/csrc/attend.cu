@@ -312,6 +312,7 @@ static cudaError_t simt_q(int kv_dtype, const AttendArgs &a, cudaStream_t s) {
 size_t attend_scratch_bytes() { return kAttendPartFloats * sizeof(float); }
 
 cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s) {
+    if (attend_decode_supported(q_dtype, kv_dtype, a)) return launch_attend_decode(kv_dtype, a, s);
     if (attend_tc_supported(q_dtype, kv_dtype, a)) return launch_attend_tc(kv_dtype, a, s);
     return q_dtype == BF16 ? simt_q<__nv_bfloat16>(kv_dtype, a, s) : simt_q<float>(kv_dtype, a, s);
 }

@@ -169,6 +169,11 @@ __host__ __device__ __forceinline__ size_t part_slot(int cta, bool first) {
 constexpr int kTileMaxCtas = 160, kTileMaxRows = 256;
 constexpr size_t kAttendPartFloats = (size_t)kTileMaxCtas * 2 * kTileMaxRows * 130;
 
+// attend_decode.cu: up to kDecodeRows query rows of a kv head, the same types.
+constexpr int kDecodeRows = 16;
+bool attend_decode_supported(int q_dtype, int kv_dtype, const AttendArgs &a);
+cudaError_t launch_attend_decode(int kv_dtype, const AttendArgs &a, cudaStream_t s);
+
 // attend_tc.cu: tensor-core tiles of 128 query rows, for bf16 queries over bf16
 // or e4m3 pages.
 bool attend_tc_supported(int q_dtype, int kv_dtype, const AttendArgs &a);
