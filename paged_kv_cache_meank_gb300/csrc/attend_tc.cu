@@ -23,7 +23,8 @@
 // tiles; with power-of-two scales every value is exact in bf16, so the rest of
 // the kernel is the bf16 one.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2-3 idle, 4-7 and 8-11 softmax, e4m3:
+// Warps: 0 TMA producer, 1 MMA issuer, 2 walks the CTA's run of the work line
+// and hands its segments to the others, 4-7 and 8-11 softmax, e4m3:
 // 12-15 convert.  Registers move to the softmax warpgroups (setmaxnreg).  One CTA
 // per SM walks an equal run of the call's work line (attend_common.cuh).
 // Every wait is bounded to a second; on timeout the device error flag (bit 4) is
@@ -53,24 +54,40 @@ struct Lay {
     static constexpr int KA = D / 64;                  // 128-byte atoms of a row
     static constexpr int ATOM = TK * 128;              // one atom of a 128-row tile
     static constexpr int TILE = KA * ATOM;             // a K, V or Q tile in bf16
-    static constexpr int SLOTS = E4 ? 4 : 5;           // bf16 K / V tiles
+    // K / V tiles in flight: bf16 pages in as many slots as fit; of e4m3 pages
+    // the raw tiles are what is in flight, the bf16 ones a hand-over
+    static constexpr int SLOTS = E4 ? 3 : D == 64 ? 8 : 5;
     static constexpr int RAW = TK * D;                 // an e4m3 K or V tile
-    static constexpr int RAW_SLOTS = E4 ? 2 : 0;
+    static constexpr int RAW_SLOTS = E4 ? (D == 64 ? 8 : 4) : 0;
     static constexpr int OFF_Q = 0;                    // two row tiles
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE;
     static constexpr int OFF_ML = OFF_RAW + RAW_SLOTS * RAW;       // SPLIT: (m, l) of group 1
     static constexpr int OFF_BAR = OFF_ML + TR * 8;
-    static constexpr int SMEM = 1024 + OFF_BAR + 256;
+    static constexpr int SMEM = 1024 + OFF_BAR + 768;
     static constexpr int THREADS = E4 ? 512 : 384;
-    static_assert(OFF_KV + SLOTS * TILE - OFF_KV >= (kMaxSeqs + 1) * 8, "prefix fits the ring");
+    static_assert(SLOTS * TILE >= (kMaxSeqs + 1) * 8, "prefix fits the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+// One segment of the CTA's run, as the roles need it.
+struct Seg {
+    int T;                      // key tiles; 0: no key is seen; -1: the run is over
+    int u0;                     // first tile
+    int s, g, q0, q_len, kv;    // sequence, kv head, its rows and lengths
+    int rbase;                  // first query row of the row tile
+    int whole, first;           // all of the tile's keys; the tile begins in this CTA
+};
+
+constexpr int kSegs = 4;        // segments handed out ahead
+
 struct Bars {
-    uint64_t full[5], empty[5], raw_full[2], raw_empty[2], s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t full[8], empty[8], raw_full[8], raw_empty[8], s_full[2], p_full[2], o_full[2], q_full[2];
+    uint64_t seg_full[kSegs], seg_empty[kSegs], meet[2];
+    Seg seg[kSegs];
     uint32_t tmem;
 };
+static_assert(sizeof(Bars) <= 768, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -80,6 +97,31 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return r;
+}
+// (a, b) * c + d and (a, b) + (c, d), two float32 per instruction.
+__device__ __forceinline__ float2 fma2(uint32_t a, uint32_t b, float c, float d) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "r"(b), "f"(c), "f"(d));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 
@@ -102,7 +144,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                    const __grid_constant__ AttendArgs a, int min_units) {
     using LY = Lay<D, E4>;
     constexpr int RB = PAIR ? 2 * TR : TR;
-    constexpr int NS = LY::SLOTS;
+    constexpr int NS = LY::SLOTS, NR = E4 ? LY::RAW_SLOTS : NS;
     constexpr uint32_t kIdescS = tc::idesc_bf16_f32(TR, TK);
     constexpr uint32_t kIdescO = tc::idesc_bf16_f32(TR, D) | tc::kIdescBMajorMn;
     extern __shared__ uint8_t smem_raw[];
@@ -111,24 +153,28 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     uint8_t *qs = smem + LY::OFF_Q, *kvs = smem + LY::OFF_KV, *raws = smem + LY::OFF_RAW;
     float2 *ml1 = reinterpret_cast<float2 *>(smem + LY::OFF_ML);
     Bars *bar = reinterpret_cast<Bars *>(smem + LY::OFF_BAR);
-    int64_t *pre = reinterpret_cast<int64_t *>(kvs);     // only until the walk has started
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-    const int cta = blockIdx.x;
     int *err = a.b.err;
 
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < 8; ++s) {
             tc::mbar_init(&bar->full[s], E4 ? 128 : 1);
             tc::mbar_init(&bar->empty[s], 1);
-        }
-        for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&bar->raw_full[s], 1);
             tc::mbar_init(&bar->raw_empty[s], 128);
+        }
+        for (int s = 0; s < 2; ++s) {
             tc::mbar_init(&bar->s_full[s], 1);
             tc::mbar_init(&bar->p_full[s], 128);
             tc::mbar_init(&bar->o_full[s], 1);
             tc::mbar_init(&bar->q_full[s], PAIR ? 128 : 256);
+            tc::mbar_init(&bar->meet[s], 256);
+        }
+        for (int s = 0; s < kSegs; ++s) {
+            tc::mbar_init(&bar->seg_full[s], 1);
+            // producer, MMA issuer, eight softmax warps, four converting warps
+            tc::mbar_init(&bar->seg_empty[s], E4 ? 14 : 10);
         }
         tc::fence_mbar_init();
     }
@@ -137,34 +183,59 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tc::tmem_relinquish();
     }
     using W = Walk<RB, TK>;
-    W::LN::lay_out(a, pre);
+    {
+        // the prefix sums live in the ring until the walk has started
+        int64_t *pre = reinterpret_cast<int64_t *>(kvs);
+        W::LN::lay_out(a, pre);
+    }
     W k;
-    const bool any = k.start(a, pre, cta, gridDim.x, min_units);
-    tc::fence_proxy_async_smem();                        // `pre` before the ring's first copies
+    bool any = false;
+    if (tid == 64)
+        any = k.start(a, reinterpret_cast<const int64_t *>(kvs), blockIdx.x, gridDim.x, min_units);
+    tc::fence_proxy_async_smem();                        // before the ring's first copies
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = bar->tmem;
     tc::launch_dependents();
 
+    // Each role takes the segments in turn: open() returns false after a wait
+    // that gave up; close() hands the place back (one arrival a role's warp).
+    auto open = [&](int n) -> const Seg * {
+        return tc::mbar_wait(&bar->seg_full[n % kSegs], (n / kSegs) & 1, kWaitNs)
+                   ? &bar->seg[n % kSegs]
+                   : nullptr;
+    };
+    auto close = [&](int n) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar->seg_empty[n % kSegs]);
+    };
+
     if (wg == 0) {
-        tc::regs_release<E4 ? 64 : 88>();
-        if (warp == 0 && any) {
+        tc::regs_release<E4 ? 64 : 72>();
+        if (warp == 0) {
             // ---------------------------------------------------- producer
             int n = 0;                                   // tiles issued: slot and parity
-            constexpr int NR = E4 ? 2 : NS;
             uint64_t *fb = E4 ? bar->raw_full : bar->full, *eb = E4 ? bar->raw_empty : bar->empty;
             bool ok = true;
-            do {
-                const int T = k.nk > 0 ? k.u1 - k.u0 : 0;
-                const int n_pages = (k.i.kv + kBlockTokens - 1) / kBlockTokens;
+            for (int sg = 0; ok; ++sg) {
+                const Seg *seg = open(sg);
+                if (!__all_sync(0xffffffffu, seg != nullptr)) {
+                    ok = false;
+                    break;
+                }
+                const int T = seg->T, u0 = seg->u0, kv_len = seg->kv, g = seg->g;
+                const int32_t *table = a.b.page_table + (int64_t)seg->s * a.b.table_stride;
+                close(sg);
+                if (T < 0) break;
+                const int n_pages = (kv_len + kBlockTokens - 1) / kBlockTokens;
                 int32_t ids = -1;
                 for (int j = 0; j < T && ok; ++j) {
                     if (j % 8 == 0) {                    // the page numbers of 8 tiles at once
-                        const int p = (k.u0 + j) * kPagesPerTile + lane;
+                        const int p = (u0 + j) * kPagesPerTile + lane;
                         ids = -1;
                         if (p < n_pages && j * kPagesPerTile + lane < T * kPagesPerTile) {
-                            ids = a.b.page_table[(int64_t)k.s * a.b.table_stride + p];
+                            ids = table[p];
                             if (ids < 0 || ids >= a.b.n_pages) {
                                 atomicOr(err, kErrBatch);
                                 ids = -1;
@@ -175,11 +246,11 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         __shfl_sync(0xffffffffu, ids, (j % 8) * kPagesPerTile + (lane & 3));
                     const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & 15u;
                     const int64_t head =
-                        page < 0 ? -1 : ((int64_t)page * a.b.L + a.b.layer) * a.b.G + k.g;
+                        page < 0 ? -1 : ((int64_t)page * a.b.L + a.b.layer) * a.b.G + g;
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const int s = n % NR;
-                        ok = tc::mbar_wait(&eb[s], ((n / NR) & 1) ^ 1, kWaitNs);
-                        if (!__all_sync(0xffffffffu, ok)) {
+                        if (!__all_sync(0xffffffffu,
+                                        tc::mbar_wait(&eb[s], ((n / NR) & 1) ^ 1, kWaitNs))) {
                             ok = false;
                             break;
                         }
@@ -204,7 +275,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         }
                     }
                 }
-            } while (ok && k.next(a));
+            }
             if (!ok && lane == 0) atomicOr(err, 4);
             // every copy issued lands before the CTA ends
             for (int i = max(0, n - NR); i < n; ++i)
@@ -212,25 +283,32 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (lane == 0) atomicOr(err, 4);
                     break;
                 }
-        } else if (warp == 1 && any) {
+        } else if (warp == 1) {
             // ---------------------------------------------------- MMA issuer
             const uint32_t qbase = tc::smem_u32(qs), kvbase = tc::smem_u32(kvs);
             int n = 0;                                   // K / V tiles of earlier segments
             uint32_t qn = 0, pn[2] = {0, 0};             // uses of q_full, p_full
+            uint32_t on[2] = {0, 0};                     // segments that ended in o_full
             bool ok = true;
             auto wait = [&](uint64_t *b, uint32_t parity) {
                 if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(b, parity, kWaitNs))) ok = false;
                 return ok;
             };
-            uint32_t on[2] = {0, 0};                     // segments that ended in o_full
-            do {
-                const int T = k.nk > 0 ? k.u1 - k.u0 : 0;
+            for (int sg = 0; ok; ++sg) {
+                const Seg *seg = open(sg);
+                if (!__all_sync(0xffffffffu, seg != nullptr)) {
+                    ok = false;
+                    break;
+                }
+                const int T = seg->T, left = seg->kv - seg->u0 * TK;
+                close(sg);
+                if (T < 0) break;
                 if (T == 0) continue;
                 // K tile j is use n + 2j of the ring, V tile j use n + 2j + 1
                 auto qk = [&](int gr, int j, bool first) {
                     const int use = n + 2 * j, s = use % NS;
                     if (!wait(&bar->full[s], (use / NS) & 1)) return;
-                    if (first && (PAIR || gr == 0) && !wait(&bar->q_full[gr], qn & 1)) return;
+                    if (first && !wait(&bar->q_full[gr], qn & 1)) return;
                     tc::tc_fence_after();
                     if (lane == 0) {
                         const uint32_t qb = qbase + (PAIR ? gr * LY::TILE : 0), kb = kvbase + s * LY::TILE;
@@ -251,7 +329,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (!wait(&bar->full[s], (use / NS) & 1)) return;
                     if (!E4 && (!PAIR || gr == 0)) {
                         // rows behind the last key may hold anything (0 * NaN): clear them
-                        const int key0 = (k.u0 + j) * TK, end = k.i.kv - key0;
+                        const int end = left - j * TK;
                         if (end < TK && (end & 31)) {
                             const int rows = 32 - (end & 31);
                             for (int i = lane; i < rows * LY::KA * 8; i += 32) {
@@ -299,69 +377,101 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 ++qn;
                 n += 2 * T;
-            } while (ok && k.next(a));
+            }
             if (!ok && lane == 0) atomicOr(err, 4);
             // the last commits cover every MMA issued: done before TMEM is freed
             for (int gr = 0; gr < 2; ++gr)
                 if (on[gr] > 0 && !tc::mbar_wait(&bar->o_full[gr], (on[gr] - 1) & 1, kWaitNs))
                     if (lane == 0) atomicOr(err, 4);
+        } else if (warp == 2 && lane == 0) {
+            // ---------------------------------------------------- the walk
+            for (int n = 0;; ++n) {
+                const int p = n % kSegs;
+                if (!tc::mbar_wait(&bar->seg_empty[p], ((n / kSegs) & 1) ^ 1, kWaitNs)) {
+                    atomicOr(err, 4);
+                    break;
+                }
+                Seg *seg = &bar->seg[p];
+                if (any) {
+                    seg->T = k.nk > 0 ? k.u1 - k.u0 : 0;
+                    seg->u0 = k.u0;
+                    seg->s = k.s;
+                    seg->g = k.g;
+                    seg->q0 = k.i.q0;
+                    seg->q_len = k.i.q_len;
+                    seg->kv = k.i.kv;
+                    seg->rbase = k.r * RB;
+                    seg->whole = k.whole();
+                    seg->first = k.first_cta() == (int)blockIdx.x;
+                } else {
+                    seg->T = -1;
+                }
+                tc::mbar_arrive(&bar->seg_full[p]);
+                if (!any) break;
+                any = k.next(a);
+            }
         }
     } else if (wg <= 2) {
         // -------------------------------------------------------- softmax
         tc::regs_take<E4 ? 176 : 208>();
-        const int gr = wg - 1, quad = warp & 3, row = quad * 32 + lane;   // row of the 128
-        const int gtid = tid - 128 - gr * 128;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const int gr = wg - 1, row = (warp & 3) * 32 + lane;              // row of the 128
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + gr * TK, to = tmem + lanes + 256 + gr * 128;
         // a negative scale turns the queries' sign, a scale of 0 clears them: c > 0
         const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-        const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
-        uint32_t sn = 0, on[2] = {0, 0};
-        // after a wait that gave up, the walk goes on without waits or work: the
-        // groups still meet at their barriers
+        uint32_t sn = 0, on = 0, on1 = 0, met = 0;
         bool ok = true;
-        bool more = any, first_seg = true;
-        while (more) {
-            const int T = k.nk > 0 ? k.u1 - k.u0 : 0;
-            const int rows_all = k.i.q_len * a.gqa, rbase = k.r * RB;
-            if (!PAIR) {
-                // group 0 has read group 1's sums, and nobody reads Q any more
-                if (!first_seg) tc::named_sync(1, 256);
+        auto meet = [&](int which) {                     // both groups (SPLIT)
+            tc::mbar_arrive(&bar->meet[which]);
+            ok = tc::mbar_wait(&bar->meet[which], met & 1, kWaitNs);
+            return ok;
+        };
+        for (int sg = 0; ok; ++sg) {
+            const Seg *seg = open(sg);
+            if (seg == nullptr) {
+                ok = false;
+                break;
             }
-            first_seg = false;
-            if (T > 0 && ok) {
-                // this group's query rows (SPLIT: its half) into the swizzled layout
-                const int r0 = PAIR ? 0 : gr * (TR / 2), r1 = PAIR ? TR : r0 + TR / 2;
-                uint8_t *dst = qs + (PAIR ? gr * LY::TILE : 0);
-                const int base = rbase + (PAIR ? gr * TR : 0);
-                for (int i = gtid; i < (r1 - r0) * (D / 8); i += 128) {
-                    const int r = r0 + i / (D / 8), c16 = i % (D / 8), qrow = base + r;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (qrow < rows_all) {
-                        const int t = qrow / a.gqa, h = qrow - t * a.gqa;
-                        v = __ldg(reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(a.q) +
-                            (int64_t)(k.i.q0 + t) * a.q_stride +
-                            (int64_t)(k.g * a.gqa + h) * D + c16 * 8));
-                        v.x = (v.x ^ flip) & keep;
-                        v.y = (v.y ^ flip) & keep;
-                        v.z = (v.z ^ flip) & keep;
-                        v.w = (v.w ^ flip) & keep;
+            const int T = seg->T;
+            if (T < 0) break;
+            int vis;
+            {
+                const int q_len = seg->q_len, kv = seg->kv, rows_all = q_len * a.gqa;
+                const int base = seg->rbase + (PAIR ? gr * TR : 0);
+                vis = a.causal ? min(kv, kv - q_len + (base + row) / a.gqa + 1) : kv;
+                if (T > 0) {
+                    // this group's query rows (SPLIT: its half) into the swizzled layout;
+                    // nobody reads the last segment's any more
+                    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+                    const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
+                    const int r0 = PAIR ? 0 : gr * (TR / 2), n_rows = PAIR ? TR : TR / 2;
+                    uint8_t *dst = qs + (PAIR ? gr * LY::TILE : 0);
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
+                                               (int64_t)seg->q0 * a.q_stride +
+                                               (int64_t)seg->g * a.gqa * D;
+                    for (int i = tid & 127; i < n_rows * (D / 8); i += 128) {
+                        const int r = r0 + i / (D / 8), c16 = i % (D / 8), qrow = base + r;
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (qrow < rows_all) {
+                            const int t = qrow / a.gqa, h = qrow - t * a.gqa;
+                            v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)t * a.q_stride +
+                                                                      h * D + c16 * 8));
+                            v.x = (v.x ^ flip) & keep;
+                            v.y = (v.y ^ flip) & keep;
+                            v.z = (v.z ^ flip) & keep;
+                            v.w = (v.w ^ flip) & keep;
+                        }
+                        *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * LY::ATOM + r * 128 +
+                                                   (((c16 & 7) ^ (r & 7)) << 4)) = v;
                     }
-                    *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * LY::ATOM + r * 128 +
-                                               (((c16 & 7) ^ (r & 7)) << 4)) = v;
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
                 }
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
+                vis -= seg->u0 * TK;                     // from the segment's first key
             }
-            const int qrow = rbase + (PAIR ? gr * TR : 0) + row;
-            const bool live = qrow < rows_all;
-            const int tok = qrow / a.gqa;
-            const int vis = a.causal ? min(k.i.kv, k.i.kv - k.i.q_len + tok + 1) : k.i.kv;
             float m = -INFINITY, l = 0.f;
-            const int step = PAIR ? 1 : 2;
-            for (int j = PAIR ? 0 : gr; j < T && ok; j += step) {
+            constexpr int step = PAIR ? 1 : 2;
+            for (int j = PAIR ? 0 : gr; j < T; j += step) {
                 if (!tc::mbar_wait(&bar->s_full[gr], sn & 1, kWaitNs)) {
                     ok = false;
                     break;
@@ -373,17 +483,21 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 for (int i = 0; i < TK; i += 32) tc::tmem_ld32_async(ts + i, s + i);
 #pragma unroll
                 for (int i = 0; i < TK; i += 16) tc::tmem_wait_ld(s + i);
-                const int key0 = (k.u0 + j) * TK;
-                if (__any_sync(0xffffffffu, key0 + TK > vis)) {
+                if (__any_sync(0xffffffffu, (j + 1) * TK > vis)) {
+                    const int seen = vis - j * TK;
 #pragma unroll
                     for (int i = 0; i < TK; ++i)
-                        if (key0 + i >= vis) s[i] = 0xFF800000u;
+                        if (i >= seen) s[i] = 0xFF800000u;
                 }
                 float mx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
 #pragma unroll
-                for (int i = 4; i < TK; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[i]));
+                for (int i = 4; i < 124; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[124 + e]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                 const float m_new = fmaxf(m, top);
                 const bool grow = m_new > m + kMoveMax || (m == -INFINITY && m_new > m);
@@ -393,53 +507,61 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
                     l *= f;
                     if (j >= step) {
-#pragma unroll
-                        for (int i = 0; i < D; i += 32) {
-                            uint32_t o[32];
-                            tc::tmem_ld32_async(to + i, o);
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t o[16];
+                            tc::tmem_ld16_async(to + i, o);
                             tc::tmem_wait_ld(o);
-                            tc::tmem_wait_ld(o + 16);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
+                            for (int e = 0; e < 16; ++e)
                                 o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::tmem_st32(to + i, o);
+                            tc::tmem_st16(to + i, o);
                         }
                     }
                     m = m_new;
                 }
                 const float off = m == -INFINITY ? 0.f : -m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
+                for (int h = 0; h < TK / 32; ++h) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x = ex2(fmaf(__uint_as_float(s[h * 64 + 2 * i]), c, off));
-                        const float y = ex2(fmaf(__uint_as_float(s[h * 64 + 2 * i + 1]), c, off));
-                        sum[(2 * i) & 3] += x;
-                        sum[(2 * i + 1) & 3] += y;
-                        p[i] = pack_bf16(x, y);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = fma2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1], c, off);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[i & 1] = add2(sum[i & 1], x);
+                        p[i] = pack_bf16(x.x, x.y);
                     }
-                    tc::tmem_st32(ts + h * 32, p);
+                    tc::tmem_st16(ts + h * 16, p);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&bar->p_full[gr]);
             }
+            if (!ok) break;
             // ------------------------------------------------ the segment's end
             const bool mine = T > (PAIR ? 0 : gr);      // this group has an O
-            if (mine && ok && !tc::mbar_wait(&bar->o_full[gr], on[gr] & 1, kWaitNs)) ok = false;
-            if (mine) ++on[gr];
+            if (mine) {
+                if (!tc::mbar_wait(&bar->o_full[gr], on & 1, kWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                ++on;
+            }
             float f0 = 1.f, f1 = 0.f;
             if (!PAIR) {
                 if (gr == 1) ml1[row] = make_float2(m, l);
-                tc::named_sync(2, 256);
+                if (!meet(0)) break;
                 if (gr == 0) {                          // group 0 writes the rows
                     const float2 o1 = ml1[row];
                     if (T > 1) {
-                        if (ok && !tc::mbar_wait(&bar->o_full[1], on[1] & 1, kWaitNs)) ok = false;
-                        ++on[1];
+                        if (!tc::mbar_wait(&bar->o_full[1], on1 & 1, kWaitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        ++on1;
                     }
                     const float mm = fmaxf(m, o1.x), base = mm == -INFINITY ? 0.f : mm;
                     f0 = ex2(m - base);
@@ -448,16 +570,25 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     m = mm;
                 }
             }
-            if (ok && (PAIR || gr == 0)) {
+            if (PAIR || gr == 0) {
                 tc::tc_fence_after();
-                const bool whole = k.whole();
-                const int prow = (PAIR ? gr * TR : 0) + row;
-                float *rec = a.part + part_slot(cta, cta == k.first_cta()) * ((size_t)RB * (D + 2));
+                const bool whole = seg->whole;
+                const int prow = (PAIR ? gr * TR : 0) + row, qrow = seg->rbase + prow;
+                const bool live = qrow < seg->q_len * a.gqa;
+                const int tok = qrow / a.gqa, h = seg->g * a.gqa + qrow - tok * a.gqa;
+                float *rec = a.part + part_slot(blockIdx.x, seg->first) * ((size_t)RB * (D + 2));
                 const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-                const int h = k.g * a.gqa + qrow - tok * a.gqa;
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                     (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D;
-#pragma unroll
+                                     (int64_t)(seg->q0 + tok) * a.out_stride + (int64_t)h * D;
+                if (whole) {
+                    if (live && a.lse)
+                        a.lse[(int64_t)(seg->q0 + tok) * a.H + h] =
+                            m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+                } else {
+                    rec[(size_t)RB * D + prow] = m;
+                    rec[(size_t)RB * (D + 1) + prow] = l;
+                }
+#pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
                     if (mine) {
@@ -497,17 +628,14 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                 make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                 }
-                if (whole) {
-                    if (live && a.lse)
-                        a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] =
-                            m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
-                } else {
-                    rec[(size_t)RB * D + prow] = m;
-                    rec[(size_t)RB * (D + 1) + prow] = l;
-                }
                 tc::tc_fence_before();
             }
-            more = k.next(a);
+            // SPLIT: Q and group 1's sums may be overwritten once both are here
+            if (!PAIR) {
+                if (!meet(1)) break;
+                ++met;
+            }
+            close(sg);
         }
         if (!ok) atomicOr(err, 4);
     } else {
@@ -516,40 +644,52 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             tc::regs_release<88>();
             const int w = warp & 3;                      // its page of the tile
             int n = 0;                                   // K / V tiles converted
-            bool ok = any;
+            bool ok = true;
             const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((120 + 127) << 23));
-            while (ok) {
-                const int T = k.nk > 0 ? k.u1 - k.u0 : 0;
-                const int n_pages = (k.i.kv + kBlockTokens - 1) / kBlockTokens;
+            for (int sg = 0; ok; ++sg) {
+                const Seg *seg = open(sg);
+                if (!__all_sync(0xffffffffu, seg != nullptr)) {
+                    ok = false;
+                    break;
+                }
+                const int T = seg->T, u0 = seg->u0, kv_len = seg->kv, g = seg->g;
+                const int64_t table = (int64_t)seg->s * a.b.table_stride;
+                close(sg);
+                if (T < 0) break;
+                float ks = 1.f, vs = 1.f;                // lane i: of the page of tile 32 x + i
+                int rows_of = 0;
                 for (int j = 0; j < T && ok; ++j) {
-                    const int p = (k.u0 + j) * kPagesPerTile + w;
-                    float sc[2] = {1.f, 1.f};
-                    bool there = false;
-                    if (p < n_pages) {
-                        const int64_t at = (int64_t)k.s * a.b.table_stride + p;
-                        const int64_t page = a.b.page_table[at];
-                        there = page >= 0 && page < a.b.n_pages;
-                        if (a.k_scale) {
-                            const int64_t r = a.b.scale_rows ? (int64_t)a.b.scale_rows[at] : page;
-                            if (r >= 0 && r < a.b.n_scale_rows) {
-                                const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + k.g;
-                                sc[0] = checked_scale(a.k_scale[so], err);
-                                sc[1] = checked_scale(a.v_scale[so], err);
-                            } else {
-                                if (lane == 0) atomicOr(err, kErrBatch);
-                                there = false;
+                    if ((j & 31) == 0) {                 // the scales of 32 tiles at once
+                        const int p = (u0 + j + lane) * kPagesPerTile + w;
+                        rows_of = 0;
+                        if (j + lane < T && p * kBlockTokens < kv_len) {
+                            const int64_t page = a.b.page_table[table + p];
+                            bool there = page >= 0 && page < a.b.n_pages;
+                            if (a.k_scale) {
+                                const int64_t r = a.b.scale_rows ? (int64_t)a.b.scale_rows[table + p] : page;
+                                if (r >= 0 && r < a.b.n_scale_rows) {
+                                    const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + g;
+                                    ks = checked_scale(a.k_scale[so], err);
+                                    vs = checked_scale(a.v_scale[so], err);
+                                } else {
+                                    atomicOr(err, kErrBatch);
+                                    there = false;
+                                }
                             }
+                            if (there) rows_of = min(kBlockTokens, kv_len - p * kBlockTokens);
                         }
                     }
-                    const int rows = there ? min(kBlockTokens, k.i.kv - p * kBlockTokens) : 0;
+                    const int rows = __shfl_sync(0xffffffffu, rows_of, j & 31);
                     for (int kv = 0; kv < 2; ++kv, ++n) {
-                        const int rs = n & 1, s = n % NS;
-                        if (!tc::mbar_wait(&bar->raw_full[rs], (n >> 1) & 1, kWaitNs) ||
-                            !tc::mbar_wait(&bar->empty[s], ((n / NS) & 1) ^ 1, kWaitNs)) {
+                        const int rs = n % NR, s = n % NS;
+                        const __nv_bfloat162 scale = __float2bfloat162_rn(
+                            __shfl_sync(0xffffffffu, kv ? vs : ks, j & 31));
+                        if (!__all_sync(0xffffffffu,
+                                        tc::mbar_wait(&bar->raw_full[rs], (n / NR) & 1, kWaitNs) &&
+                                            tc::mbar_wait(&bar->empty[s], ((n / NS) & 1) ^ 1, kWaitNs))) {
                             ok = false;
                             break;
                         }
-                        const __nv_bfloat162 scale = __float2bfloat162_rn(sc[kv]);
                         const uint8_t *src = raws + rs * LY::RAW + w * kBlockTokens * D;
                         uint8_t *dst = kvs + s * LY::TILE;
                         constexpr int CPR = D / 16;      // 16-byte pieces of a raw row
@@ -589,9 +729,8 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         tc::mbar_arrive(&bar->full[s]);
                     }
                 }
-                if (!ok || !k.next(a)) break;
             }
-            if (any && !ok) atomicOr(err, 4);
+            if (!ok) atomicOr(err, 4);
         }
     }
     tc::tc_fence_before();
