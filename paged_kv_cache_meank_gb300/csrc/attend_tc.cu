@@ -300,7 +300,9 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     ok = false;
                     break;
                 }
-                const int T = seg->T, left = seg->kv - seg->u0 * TK;
+                // uniform over the warp, and known to be: descriptors stay in uniform registers
+                const int T = __shfl_sync(0xffffffffu, seg->T, 0);
+                const int left = __shfl_sync(0xffffffffu, seg->kv - seg->u0 * TK, 0);
                 close(sg);
                 if (T < 0) break;
                 if (T == 0) continue;
@@ -310,15 +312,15 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (!wait(&bar->full[s], (use / NS) & 1)) return;
                     if (first && !wait(&bar->q_full[gr], qn & 1)) return;
                     tc::tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t qb = qbase + (PAIR ? gr * LY::TILE : 0), kb = kvbase + s * LY::TILE;
+                    const uint32_t qb = tc::desc_lo(qbase + (PAIR ? gr * LY::TILE : 0), 16);
+                    const uint32_t kb = tc::desc_lo(kvbase + s * LY::TILE, 16);
+                    if (tc::elect_one()) {
 #pragma unroll
-                        for (int at = 0; at < LY::KA; ++at)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc::mma_bf16(tmem + gr * TK, tc::sdesc_sw128(qb + at * LY::ATOM + kk * 32),
-                                             tc::sdesc_sw128(kb + at * LY::ATOM + kk * 32), kIdescS,
-                                             (at | kk) != 0);
+                        for (int x = 0; x < 4 * LY::KA; ++x) {
+                            const uint32_t at = ((x >> 2) * LY::ATOM + (x & 3) * 32) >> 4;
+                            tc::mma_16_ss(tmem + gr * TK, qb + at, tc::kDescHiSw128, kb + at,
+                                          tc::kDescHiSw128, kIdescS, x != 0);
+                        }
                         if (!PAIR || gr == 1) tc::mma_commit(&bar->empty[s]);
                         tc::mma_commit(&bar->s_full[gr]);
                     }
@@ -345,13 +347,13 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (!wait(&bar->p_full[gr], pn[gr] & 1)) return;
                     ++pn[gr];
                     tc::tc_fence_after();
-                    if (lane == 0) {
-                        const uint32_t vb = kvbase + s * LY::TILE;
+                    const uint32_t vb = tc::desc_lo(kvbase + s * LY::TILE, LY::ATOM);
+                    if (tc::elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < TK / 16; ++kk)
-                            tc::mma_bf16_ta(tmem + 256 + gr * 128, tmem + gr * TK + kk * 8,
-                                            tc::sdesc_sw128_mn(vb + kk * 16 * 128, LY::ATOM), kIdescO,
-                                            !first || kk != 0);
+                            tc::mma_16_ts(tmem + 256 + gr * 128, tmem + gr * TK + kk * 8,
+                                          vb + (kk * 16 * 128 >> 4), tc::kDescHiSw128, kIdescO,
+                                          !first || kk != 0);
                         if (!PAIR || gr == 1) tc::mma_commit(&bar->empty[s]);
                         if (last) tc::mma_commit(&bar->o_full[gr]);
                     }
