@@ -47,40 +47,73 @@ struct Line {
     __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, int gqa, int causal, int r) {
         return max(1, (keys(i, gqa, causal, r) + UNIT - 1) / UNIT);
     }
-    // pre[s] = units of the sequences before s (pre: kMaxSeqs + 1 in shared
-    // memory).  Called by the whole CTA; ends with a barrier.
+    // pre[s] = units of the sequences before s, pre[n_seqs] = all, pre[n_seqs + 1]
+    // = the largest tile's (pre: kMaxSeqs + 2 in shared memory).  By one warp.
     __device__ static void lay_out(const AttendArgs &a, int64_t *pre) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-        for (int s = warp; s < a.b.n_seqs; s += warps) {
-            bool ok;
-            const SeqInfo i = seq_info(a.b, s, &ok);
-            if (!ok && lane == 0) atomicOr(a.b.err, kErrBatch);
-            int64_t w = 0;
+        const int lane = threadIdx.x & 31;
+        int64_t run = 0;
+        int most = 1;
+        for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
+            const int s = s0 + lane;
+            SeqInfo i{0, 0, 0};
+            bool ok = true;
+            if (s < a.b.n_seqs) i = seq_info(a.b, s, &ok);
+            if (!ok) atomicOr(a.b.err, kErrBatch);
             const int n = tiles(i, a.gqa);
-            for (int r = lane; r < n; r += 32) w += weight(i, a.gqa, a.causal, r);
+            int64_t w = 0;
+            // few tiles each: a lane sums its sequence's; many: the warp takes the
+            // sequences in turn
+            if (__all_sync(0xffffffffu, n <= 8)) {
+                for (int r = 0; r < n; ++r) w += weight(i, a.gqa, a.causal, r);
+            } else {
+                for (int x = 0; x < min(32, a.b.n_seqs - s0); ++x) {
+                    SeqInfo j;
+                    j.q0 = 0;
+                    j.q_len = __shfl_sync(0xffffffffu, i.q_len, x);
+                    j.kv = __shfl_sync(0xffffffffu, i.kv, x);
+                    const int m = tiles(j, a.gqa);
+                    int64_t sum = 0;
+                    for (int r = lane; r < m; r += 32) sum += weight(j, a.gqa, a.causal, r);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-            if (lane == 0) pre[s + 1] = w * a.b.G;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            int64_t run = 0;
-            for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
-                const int s = s0 + lane;
-                int64_t w = s < a.b.n_seqs ? pre[s + 1] : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
-                    if (lane >= o) w += up;
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == x) w = sum;
                 }
-                if (s < a.b.n_seqs) pre[s + 1] = run + w;
-                run += __shfl_sync(0xffffffffu, w, 31);
             }
-            if (lane == 0) pre[0] = 0;
+            if (n > 0) most = max(most, weight(i, a.gqa, a.causal, n - 1));   // the last sees most
+            w *= a.b.G;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w += up;
+            }
+            if (s < a.b.n_seqs) pre[s + 1] = run + w;
+            run += __shfl_sync(0xffffffffu, w, 31);
         }
-        __syncthreads();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (lane == 0) {
+            pre[0] = 0;
+            pre[a.b.n_seqs + 1] = most;
+        }
+        __syncwarp();
     }
 };
+
+// a / b, both >= 0: 32-bit division where they fit (a 64-bit one takes about 10
+// times as long, and a walk has several before its first load).
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Units of one CTA's run: an equal share, but not so small that a tile's join
+// costs more than its keys, unless whole tiles are smaller.
+__host__ __device__ __forceinline__ int64_t run_units(const AttendArgs &a, const int64_t *pre, int n_ctas,
+                                                      int min_units) {
+    const int64_t share = quotient(pre[a.b.n_seqs] + n_ctas - 1, n_ctas);
+    const int64_t most = pre[a.b.n_seqs + 1], least = most < min_units ? most : min_units;
+    return share > least ? share : least;
+}
 
 // A walk over one CTA's run of the line.
 template <int RB, int UNIT>
@@ -96,7 +129,7 @@ struct Walk {
     __host__ __device__ __forceinline__ bool start(const AttendArgs &a, const int64_t *pre, int cta,
                                           int n_ctas, int min_units) {
         const int64_t total = pre[a.b.n_seqs];
-        per = max((int64_t)min_units, (total + n_ctas - 1) / n_ctas);
+        per = run_units(a, pre, n_ctas, min_units);
         if (cta * per >= total) return false;
         start_at(a, pre, cta * per, per);
         end = min(total, x + per);
@@ -119,8 +152,8 @@ struct Walk {
         i = seq_info(a.b, s, &ok);
         n_tiles = LN::tiles(i, a.gqa);
         int64_t rem = x - pre[s];
-        const int64_t per_head = (pre[s + 1] - pre[s]) / a.b.G;
-        g = (int)(rem / per_head);
+        const int64_t per_head = quotient(pre[s + 1] - pre[s], a.b.G);
+        g = (int)quotient(rem, per_head);
         rem -= g * per_head;
         r = 0;
         for (w = LN::weight(i, a.gqa, a.causal, 0); rem >= w; w = LN::weight(i, a.gqa, a.causal, r)) {
@@ -155,8 +188,8 @@ struct Walk {
     }
     __host__ __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == w; }
     // The first and last CTA that share the segment's tile.
-    __host__ __device__ __forceinline__ int first_cta() const { return (int)((x - u0) / per); }
-    __host__ __device__ __forceinline__ int last_cta() const { return (int)((x - u0 + w - 1) / per); }
+    __host__ __device__ __forceinline__ int first_cta() const { return (int)quotient(x - u0, per); }
+    __host__ __device__ __forceinline__ int last_cta() const { return (int)quotient(x - u0 + w - 1, per); }
 };
 
 // A CTA's two places for partial results: 1 for a tile that goes on in the next

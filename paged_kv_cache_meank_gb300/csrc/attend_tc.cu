@@ -4,7 +4,7 @@
 // Per kv head, the query rows (token, head of the group) of a sequence are cut
 // into tiles of 128; a unit of work is one tile of 128 keys (4 pages).  With S
 // and O of a row tile in tensor memory, a unit is
-//   S = Q K^T            M = 128 rows, N = 128 keys, both operands in shared memory
+//   S = Q K^T            M = 128 rows, N = 64 keys at a time, operands in shared memory
 //   p = 2^(S c - m)      online softmax in log2 units, c = softmax_scale log2 e
 //   O += P V             M = 128 rows, N = d; P (bf16) in tensor memory over S, V
 //                        read from its [key][d] storage as an MN-major operand
@@ -19,11 +19,13 @@
 // few times per row and not per tile.  Weights are rounded to bf16 for the
 // product with V; the running weight sums the unrounded float32.
 //
-// e4m3 pages: a fourth warpgroup turns each page into the same swizzled bf16
-// tiles; with power-of-two scales every value is exact in bf16, so the rest of
-// the kernel is the bf16 one.
+// e4m3 pages: a fourth warpgroup turns each page's codes into the same swizzled
+// tiles in f16 (exact, one instruction for two codes), and the products run in
+// f16.  q is divided by a power of two per row first; k_scale goes into the
+// factor of the page's scores; the weights times v_scale are kept in f16 against a
+// running maximum of their own, so scales of any size keep their precision.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2 walks the CTA's run of the work line
+// Warps: 0 TMA producer, 1 and 3 MMA issuers (one for each group), 2 walks the CTA's run of the work line
 // and hands its segments to the others, 4-7 and 8-11 softmax, e4m3:
 // 12-15 convert.  Registers move to the softmax warpgroups (setmaxnreg).  One CTA
 // per SM walks an equal run of the call's work line (attend_common.cuh).
@@ -42,31 +44,36 @@ namespace kvm {
 namespace {
 
 constexpr int TK = 128;                     // keys of a tile
+constexpr int HK = TK / 2;                  // keys of half a tile
 constexpr int TR = 128;                     // query rows of a tile
 constexpr int kPagesPerTile = TK / kBlockTokens;
 constexpr uint32_t kWaitNs = 1000000000u;   // 1 s
+constexpr int kMinTiles = 8;                // of a CTA's run: below, a join costs more than the keys
 constexpr float kMoveMax = 8.f;             // log2 units a tile may exceed m by
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, bool E4>
+template <int D, bool E4, bool PAIR>
 struct Lay {
     static constexpr int KA = D / 64;                  // 128-byte atoms of a row
     static constexpr int ATOM = TK * 128;              // one atom of a 128-row tile
     static constexpr int TILE = KA * ATOM;             // a K, V or Q tile in bf16
+    static constexpr int Q_TILES = PAIR ? 2 : 1;
     // K / V tiles in flight: bf16 pages in as many slots as fit; of e4m3 pages
-    // the raw tiles are what is in flight, the bf16 ones a hand-over
-    static constexpr int SLOTS = E4 ? 3 : D == 64 ? 8 : 5;
+    // the raw tiles are what is in flight, the f16 ones a hand-over.  SPLIT needs
+    // four: a group meets K of its next tile (two on) before it is done with V.
+    static constexpr int SLOTS = E4 ? (D == 64 ? 6 : PAIR ? 3 : 4) : D == 64 ? 8 : PAIR ? 5 : 6;
     static constexpr int RAW = TK * D;                 // an e4m3 K or V tile
     static constexpr int RAW_SLOTS = E4 ? (D == 64 ? 8 : 4) : 0;
-    static constexpr int OFF_Q = 0;                    // two row tiles
-    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = Q_TILES * TILE;
     static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE;
-    static constexpr int OFF_ML = OFF_RAW + RAW_SLOTS * RAW;       // SPLIT: (m, l) of group 1
-    static constexpr int OFF_BAR = OFF_ML + TR * 8;
-    static constexpr int SMEM = 1024 + OFF_BAR + 768;
+    static constexpr int OFF_ML = OFF_RAW + RAW_SLOTS * RAW;       // SPLIT: group 1's sums
+    static constexpr int OFF_BAR = OFF_ML + (PAIR ? 0 : TR * 12);
+    static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
-    static_assert(SLOTS * TILE >= (kMaxSeqs + 1) * 8, "prefix fits the ring");
+    static_assert(SLOTS * TILE >= (kMaxSeqs + 2) * 8, "prefix fits the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -77,17 +84,21 @@ struct Seg {
     int s, g, q0, q_len, kv;    // sequence, kv head, its rows and lengths
     int rbase;                  // first query row of the row tile
     int whole, first;           // all of the tile's keys; the tile begins in this CTA
+    int c0, n_ctas;             // the CTAs that share the tile: the first, how many
 };
 
 constexpr int kSegs = 4;        // segments handed out ahead
+constexpr int kScales = 4;      // tiles whose pages' scales are kept (see the converter)
 
 struct Bars {
-    uint64_t full[8], empty[8], raw_full[8], raw_empty[8], s_full[2], p_full[2], o_full[2], q_full[2];
-    uint64_t seg_full[kSegs], seg_empty[kSegs], meet[2];
+    uint64_t full[8], empty[8], raw_full[8], raw_empty[8], s_full[2][2], p_full[2][2], pv_done[2][2], sb_free[2], o_full[2], q_full[2];
+    uint64_t seg_full[kSegs], seg_empty[kSegs], meet[2], v_clear[8], sc_full[kScales];
     Seg seg[kSegs];
+    float2 scale[kScales][kPagesPerTile];   // e4m3: (k_scale, v_scale) of a tile's pages
     uint32_t tmem;
+    int go;
 };
-static_assert(sizeof(Bars) <= 768, "barriers");
+static_assert(sizeof(Bars) <= 1024, "barriers");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -125,79 +136,185 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
-// Two e4m3 codes in bytes 1 and 3 of t (bytes 0 and 2 zero) as bf16x2 times
-// mul.  The code's exponent and mantissa land in bf16's as a value 2^-120 times
-// its own (subnormals too), which mul restores together with the block's scale:
-// exact for every code and every power-of-two scale that keeps bf16's range.
-__device__ __forceinline__ uint32_t e4m3_bf16(uint32_t t, __nv_bfloat162 up, __nv_bfloat162 scale) {
-    const uint32_t r = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
-    __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&r);
-    v = __hmul2(__hmul2(v, up), scale);
-    return *reinterpret_cast<uint32_t *>(&v);
+__device__ __forceinline__ float2 mul2(float2 a, float c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Two e4m3 codes (low 16 bits) as f16x2: exact.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+
+// The largest biased exponent of 8 bf16, and the power of two that a query row
+// with that largest exponent is divided by on its way to f16 (kept where it and
+// its inverse are normal float32; none for a row of zeros).
+__device__ __forceinline__ int max_exponent(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t e = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e = max(e, max(w[i] & 0x7F80u, (w[i] >> 16) & 0x7F80u));
+    return (int)(e >> 7);
+}
+__device__ __forceinline__ int row_exponent(int biased) {
+    return biased == 0 ? 0 : min(126, max(-126, biased - 127));
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ uint32_t f16_of_bf16(uint32_t two, float f) {
+    return pack_f16(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xFFFF0000u) * f);
+}
+
+// U row quads (x, x + 256, ...) of a shared tile's rows [r0, r0 + nr): the
+// parts' sums joined in CTA order against a running maximum, P parts' loads in
+// flight at a time (a load of what another SM has just written takes about 1000
+// cycles).
+template <int D, int RB, int U, int P>
+__device__ __forceinline__ void join_quads(const AttendArgs &a, const Seg &sh, int r0, int nr, int x) {
+    constexpr size_t REC = (size_t)RB * (D + 2);
+    const int n = sh.n_ctas, last = nr * (D / 4) - 1;
+    int row[U], q[U];
+    float m[U], l[U];
+    float4 o[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = min(x + u * 256, last);
+        q[u] = i / nr;
+        row[u] = r0 + i - q[u] * nr;
+        m[u] = -INFINITY;
+        l[u] = 0.f;
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int p0 = 0; p0 < n; p0 += P) {
+        float pm[P][U], pl[P][U];
+        float4 v[P][U];
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int pp = min(p0 + p, n - 1);
+            const float *r = a.part + part_slot(sh.c0 + pp, pp == 0) * REC;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                pm[p][u] = __ldcg(r + (size_t)RB * D + row[u]);
+                pl[p][u] = __ldcg(r + (size_t)RB * (D + 1) + row[u]);
+                v[p][u] = __ldcg(reinterpret_cast<const float4 *>(r) + (size_t)q[u] * RB + row[u]);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (p0 + p >= n) continue;
+                const float mm = fmaxf(m[u], pm[p][u]), base = mm == -INFINITY ? 0.f : mm;
+                const float f = ex2(m[u] - base), w = ex2(pm[p][u] - base);
+                m[u] = mm;
+                l[u] = l[u] * f + pl[p][u] * w;
+                o[u].x = o[u].x * f + v[p][u].x * w;
+                o[u].y = o[u].y * f + v[p][u].y * w;
+                o[u].z = o[u].z * f + v[p][u].z * w;
+                o[u].w = o[u].w * f + v[p][u].w * w;
+            }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (x + u * 256 > last) continue;
+        const float inv = l[u] > 0.f ? 1.f / l[u] : (l[u] == 0.f ? 0.f : l[u]);
+        const int qrow = sh.rbase + row[u], tok = qrow / a.gqa, h = sh.g * a.gqa + qrow - tok * a.gqa;
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                   (int64_t)(sh.q0 + tok) * a.out_stride + (int64_t)h * D + q[u] * 4) =
+            make_uint2(pack_bf16(o[u].x * inv, o[u].y * inv), pack_bf16(o[u].z * inv, o[u].w * inv));
+        if (q[u] == 0 && a.lse)
+            a.lse[(int64_t)(sh.q0 + tok) * a.H + h] =
+                m[u] == -INFINITY ? -INFINITY : m[u] * kLn2 + logf(l[u]);
+    }
+}
+
+// This CTA's share (the part-th of n_ctas) of a shared tile's rows, by 256 threads.
+template <int D, int RB>
+__device__ __forceinline__ void join_rows(const AttendArgs &a, const Seg &sh, int part, int t) {
+    const int rows = min(RB, sh.q_len * a.gqa - sh.rbase), n = sh.n_ctas;
+    const int r0 = rows * part / n, nr = rows * (part + 1) / n - r0;
+    if (n <= 4)
+        for (int x = t; x < nr * (D / 4); x += 256 * 4) join_quads<D, RB, 4, 2>(a, sh, r0, nr, x);
+    else
+        for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 5>(a, sh, r0, nr, x);
 }
 
 }  // namespace
 
 template <int D, bool E4, bool PAIR>
-__global__ void __launch_bounds__(Lay<D, E4>::THREADS, 1)
+__global__ void __launch_bounds__(Lay<D, E4, PAIR>::THREADS, 1)
 attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ AttendArgs a, int min_units) {
-    using LY = Lay<D, E4>;
+    using LY = Lay<D, E4, PAIR>;
     constexpr int RB = PAIR ? 2 * TR : TR;
     constexpr int NS = LY::SLOTS, NR = E4 ? LY::RAW_SLOTS : NS;
-    constexpr uint32_t kIdescS = tc::idesc_bf16_f32(TR, TK);
-    constexpr uint32_t kIdescO = tc::idesc_bf16_f32(TR, D) | tc::kIdescBMajorMn;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    constexpr uint32_t kF16 = E4 ? tc::kIdescF16 : 0u;
+    constexpr uint32_t kIdescS = tc::idesc_bf16_f32(TR, HK) & ~kF16;
+    constexpr uint32_t kIdescO = (tc::idesc_bf16_f32(TR, D) & ~kF16) | tc::kIdescBMajorMn;
+    // the swizzled tiles need 1024-byte alignment, which the start of shared
+    // memory has while the kernel declares no static array
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *qs = smem + LY::OFF_Q, *kvs = smem + LY::OFF_KV, *raws = smem + LY::OFF_RAW;
     float2 *ml1 = reinterpret_cast<float2 *>(smem + LY::OFF_ML);
+    float *mp1 = reinterpret_cast<float *>(ml1 + TR);
     Bars *bar = reinterpret_cast<Bars *>(smem + LY::OFF_BAR);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
     int *err = a.b.err;
 
+    if (tc::smem_u32(smem) & 1023) {
+        if (tid == 0) atomicOr(err, 4);
+        return;
+    }
     if (tid == 0) {
         for (int s = 0; s < 8; ++s) {
             tc::mbar_init(&bar->full[s], E4 ? 128 : 1);
-            tc::mbar_init(&bar->empty[s], 1);
+            tc::mbar_init(&bar->empty[s], PAIR ? 2 : 1);
+            tc::mbar_init(&bar->v_clear[s], 1);
             tc::mbar_init(&bar->raw_full[s], 1);
             tc::mbar_init(&bar->raw_empty[s], 128);
         }
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(&bar->s_full[s], 1);
-            tc::mbar_init(&bar->p_full[s], 128);
+            for (int h = 0; h < 2; ++h) {
+                tc::mbar_init(&bar->s_full[s][h], 1);
+                tc::mbar_init(&bar->p_full[s][h], 128);
+                tc::mbar_init(&bar->pv_done[s][h], 1);
+            }
+            tc::mbar_init(&bar->sb_free[s], 128);
             tc::mbar_init(&bar->o_full[s], 1);
             tc::mbar_init(&bar->q_full[s], PAIR ? 128 : 256);
             tc::mbar_init(&bar->meet[s], 256);
         }
+        for (int s = 0; s < kScales; ++s) tc::mbar_init(&bar->sc_full[s], kPagesPerTile);
         for (int s = 0; s < kSegs; ++s) {
             tc::mbar_init(&bar->seg_full[s], 1);
-            // producer, MMA issuer, eight softmax warps, four converting warps
-            tc::mbar_init(&bar->seg_empty[s], E4 ? 14 : 10);
+            // producer, MMA issuers, eight softmax warps, four converting warps
+            tc::mbar_init(&bar->seg_empty[s], E4 ? 15 : 11);
         }
         tc::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0 && !E4) {
+        tc::prefetch_map(&kmap);
+        tc::prefetch_map(&vmap);
     }
     if (warp == 1) {
         tc::tmem_alloc(&bar->tmem, 512);
         tc::tmem_relinquish();
     }
-    using W = Walk<RB, TK>;
-    {
-        // the prefix sums live in the ring until the walk has started
-        int64_t *pre = reinterpret_cast<int64_t *>(kvs);
-        W::LN::lay_out(a, pre);
-    }
-    W k;
-    bool any = false;
-    if (tid == 64)
-        any = k.start(a, reinterpret_cast<const int64_t *>(kvs), blockIdx.x, gridDim.x, min_units);
-    tc::fence_proxy_async_smem();                        // before the ring's first copies
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = bar->tmem;
-    tc::launch_dependents();
 
     // Each role takes the segments in turn: open() returns false after a wait
     // that gave up; close() hands the place back (one arrival a role's warp).
@@ -283,13 +400,20 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (lane == 0) atomicOr(err, 4);
                     break;
                 }
-        } else if (warp == 1) {
-            // ---------------------------------------------------- MMA issuer
-            const uint32_t qbase = tc::smem_u32(qs), kvbase = tc::smem_u32(kvs);
+        } else if (warp != 2) {
+            // ---------------------------------------------------- MMA issuers
+            // One warp for each group: issuing blocks while the tensor pipe is full, so
+            // one warp's waits hide behind the other's products.
+            const int gr = warp == 1 ? 0 : 1;
+            const uint32_t qbase = tc::smem_u32(qs) + (PAIR ? gr * LY::TILE : 0), kvbase = tc::smem_u32(kvs);
+            const uint32_t ts = tmem + gr * TK, to = tmem + 256 + gr * 128;
+            uint64_t *q_full = &bar->q_full[PAIR ? gr : 0];
+            constexpr int step = PAIR ? 1 : 2;
             int n = 0;                                   // K / V tiles of earlier segments
-            uint32_t qn = 0, pn[2] = {0, 0};             // uses of q_full, p_full
-            uint32_t on[2] = {0, 0};                     // segments that ended in o_full
+            uint32_t qn = 0, pn = 0, on = 0;             // uses of q_full, p_full, o_full
+            uint32_t cleared = 0;                        // parity of each slot's v_clear
             bool ok = true;
+            // a warp-wide wait: false once one has given up
             auto wait = [&](uint64_t *b, uint32_t parity) {
                 if (ok && !__all_sync(0xffffffffu, tc::mbar_wait(b, parity, kWaitNs))) ok = false;
                 return ok;
@@ -305,113 +429,141 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int left = __shfl_sync(0xffffffffu, seg->kv - seg->u0 * TK, 0);
                 close(sg);
                 if (T < 0) break;
-                if (T == 0) continue;
-                // K tile j is use n + 2j of the ring, V tile j use n + 2j + 1
-                auto qk = [&](int gr, int j, bool first) {
-                    const int use = n + 2 * j, s = use % NS;
-                    if (!wait(&bar->full[s], (use / NS) & 1)) return;
-                    if (first && !wait(&bar->q_full[gr], qn & 1)) return;
+                const int j0 = PAIR ? 0 : gr;
+                // K tile j is use n + 2j of the ring, V tile j use n + 2j + 1.  A wait by
+                // parity means its phase only if the one before is known to be over, so
+                // every phase is waited for in turn, the other group's tiles (SPLIT) too.
+                auto filled = [&](int use) { return wait(&bar->full[use % NS], (use / NS) & 1); };
+                // scores of half of key tile j, into the 64 columns at `col`
+                auto qk = [&](int j, int half, uint32_t col) {
+                    const int s = (n + 2 * j) % NS;
                     tc::tc_fence_after();
-                    const uint32_t qb = tc::desc_lo(qbase + (PAIR ? gr * LY::TILE : 0), 16);
-                    const uint32_t kb = tc::desc_lo(kvbase + s * LY::TILE, 16);
+                    const uint32_t qb = tc::desc_lo(qbase, 16);
+                    const uint32_t kb = tc::desc_lo(kvbase + s * LY::TILE + half * HK * 128, 16);
                     if (tc::elect_one()) {
 #pragma unroll
                         for (int x = 0; x < 4 * LY::KA; ++x) {
                             const uint32_t at = ((x >> 2) * LY::ATOM + (x & 3) * 32) >> 4;
-                            tc::mma_16_ss(tmem + gr * TK, qb + at, tc::kDescHiSw128, kb + at,
-                                          tc::kDescHiSw128, kIdescS, x != 0);
+                            tc::mma_16_ss(ts + col, qb + at, tc::kDescHiSw128, kb + at, tc::kDescHiSw128,
+                                          kIdescS, x != 0);
                         }
-                        if (!PAIR || gr == 1) tc::mma_commit(&bar->empty[s]);
-                        tc::mma_commit(&bar->s_full[gr]);
+                        tc::mma_commit(&bar->s_full[gr][half]);
+                        if (half == 1) tc::mma_commit(&bar->empty[s]);
                     }
                     __syncwarp();
                 };
-                auto pv = [&](int gr, int j, bool first, bool last) {
-                    const int use = n + 2 * j + 1, s = use % NS;
-                    if (!wait(&bar->full[s], (use / NS) & 1)) return;
-                    if (!E4 && (!PAIR || gr == 0)) {
-                        // rows behind the last key may hold anything (0 * NaN): clear them
-                        const int end = left - j * TK;
-                        if (end < TK && (end & 31)) {
-                            const int rows = 32 - (end & 31);
-                            for (int i = lane; i < rows * LY::KA * 8; i += 32) {
-                                const int row = end + i / (LY::KA * 8), c = i % (LY::KA * 8);
-                                *reinterpret_cast<uint4 *>(kvs + s * LY::TILE + (c >> 3) * LY::ATOM +
-                                                           row * 128 + (c & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            }
-                            tc::fence_proxy_async_smem();
-                            __syncwarp();
-                        }
-                    }
-                    if (!wait(&bar->p_full[gr], pn[gr] & 1)) return;
-                    ++pn[gr];
+                // the half's weights (32 columns at `col`) times its half of V tile j
+                auto pv = [&](int j, int half, uint32_t col) {
+                    const int s = (n + 2 * j + 1) % NS;
                     tc::tc_fence_after();
-                    const uint32_t vb = tc::desc_lo(kvbase + s * LY::TILE, LY::ATOM);
+                    const uint32_t vb = tc::desc_lo(kvbase + s * LY::TILE + half * HK * 128, LY::ATOM);
                     if (tc::elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < TK / 16; ++kk)
-                            tc::mma_16_ts(tmem + 256 + gr * 128, tmem + gr * TK + kk * 8,
-                                          vb + (kk * 16 * 128 >> 4), tc::kDescHiSw128, kIdescO,
-                                          !first || kk != 0);
-                        if (!PAIR || gr == 1) tc::mma_commit(&bar->empty[s]);
-                        if (last) tc::mma_commit(&bar->o_full[gr]);
+                        for (int x = 0; x < HK / 16; ++x)
+                            tc::mma_16_ts(to, ts + col + x * 8, vb + (x * 16 * 128 >> 4), tc::kDescHiSw128,
+                                          kIdescO, j != j0 || half != 0 || x != 0);
+                        tc::mma_commit(&bar->pv_done[gr][half]);
+                        if (half == 1) {
+                            tc::mma_commit(&bar->empty[s]);
+                            if (j + step >= T) tc::mma_commit(&bar->o_full[gr]);
+                        }
                     }
                     __syncwarp();
-                    if (last) ++on[gr];
                 };
-                if (PAIR) {
-                    qk(0, 0, true);
-                    if (ok) qk(1, 0, true);
-                    for (int j = 0; j < T && ok; ++j)
-                        for (int gr = 0; gr < 2 && ok; ++gr) {
-                            pv(gr, j, j == 0, j == T - 1);
-                            if (ok && j + 1 < T) qk(gr, j + 1, false);
+                // rows of V tile j behind the last key may hold anything (0 * NaN): one of
+                // the tile's issuers clears them
+                auto clear_tail = [&](int j) {
+                    const int end = left - j * TK, s = (n + 2 * j + 1) % NS;
+                    if (E4 || end >= TK || !(end & 31)) return true;
+                    if (!PAIR || gr == 0) {
+                        const int rows = 32 - (end & 31);
+                        for (int i = lane; i < rows * LY::KA * 8; i += 32) {
+                            const int row = end + i / (LY::KA * 8), c = i % (LY::KA * 8);
+                            *reinterpret_cast<uint4 *>(kvs + s * LY::TILE + (c >> 3) * LY::ATOM + row * 128 +
+                                                       (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                } else {
-                    qk(0, 0, true);
-                    if (ok && T > 1) qk(1, 1, false);
-                    for (int j = 0; j < T && ok; ++j) {
-                        const int gr = j & 1;
-                        pv(gr, j, j < 2, j + 2 >= T);
-                        if (ok && j + 2 < T) qk(gr, j + 2, false);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (PAIR && lane == 0) tc::mbar_arrive(&bar->v_clear[s]);
+                    } else if (!wait(&bar->v_clear[s], cleared >> s & 1)) {
+                        return false;
+                    }
+                    cleared ^= 1u << s;
+                    return true;
+                };
+                if (T > 0 && wait(q_full, qn & 1)) {
+                    ++qn;
+                    if (j0 > 0 && (!filled(n) || !filled(n + 1))) break;
+                    if (j0 < T) {
+                        if (!filled(n + 2 * j0)) break;
+                        qk(j0, 0, HK);
+                        qk(j0, 1, 0);
+                    }
+                    // The 128 columns of S: a tile's first half lies where the last tile's
+                    // second half was, free once that is in registers, and its second where
+                    // the last tile's weights were.  So the next scores are under way while
+                    // these are weighed.  Weights take the place of the first half.
+                    uint32_t a_col = HK;
+                    for (int j = j0; j < T; j += step, a_col ^= HK) {
+                        const bool next = j + step < T;
+                        if (!filled(n + 2 * j + 1) || !clear_tail(j)) break;
+                        if (!wait(&bar->p_full[gr][0], pn & 1)) break;
+                        pv(j, 0, a_col);
+                        if (!PAIR && j + 1 < T && (!filled(n + 2 * j + 2) || !filled(n + 2 * j + 3))) break;
+                        if (next && !filled(n + 2 * (j + step))) break;
+                        if (!wait(&bar->sb_free[gr], pn & 1)) break;
+                        if (next) qk(j + step, 0, a_col ^ HK);
+                        if (!wait(&bar->p_full[gr][1], pn & 1)) break;
+                        pv(j, 1, a_col + HK / 2);
+                        if (next) qk(j + step, 1, a_col);
+                        ++pn;
+                        if (!next) ++on;
                     }
                 }
-                ++qn;
                 n += 2 * T;
             }
             if (!ok && lane == 0) atomicOr(err, 4);
-            // the last commits cover every MMA issued: done before TMEM is freed
-            for (int gr = 0; gr < 2; ++gr)
-                if (on[gr] > 0 && !tc::mbar_wait(&bar->o_full[gr], (on[gr] - 1) & 1, kWaitNs))
-                    if (lane == 0) atomicOr(err, 4);
-        } else if (warp == 2 && lane == 0) {
+            // the last commit covers every MMA issued: done before TMEM is freed
+            if (on > 0 && !tc::mbar_wait(&bar->o_full[gr], (on - 1) & 1, kWaitNs))
+                if (lane == 0) atomicOr(err, 4);
+        } else if (warp == 2) {
             // ---------------------------------------------------- the walk
-            for (int n = 0;; ++n) {
-                const int p = n % kSegs;
-                if (!tc::mbar_wait(&bar->seg_empty[p], ((n / kSegs) & 1) ^ 1, kWaitNs)) {
-                    atomicOr(err, 4);
-                    break;
+            using W = Walk<RB, TK>;
+            // the prefix sums live in the ring: its first copies follow the first segment
+            int64_t *pre = reinterpret_cast<int64_t *>(kvs);
+            W::LN::lay_out(a, pre);
+            W k;
+            bool any = k.start(a, pre, blockIdx.x, gridDim.x, min_units);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                for (int n = 0;; ++n) {
+                    const int p = n % kSegs;
+                    if (!tc::mbar_wait(&bar->seg_empty[p], ((n / kSegs) & 1) ^ 1, kWaitNs)) {
+                        atomicOr(err, 4);
+                        break;
+                    }
+                    Seg *seg = &bar->seg[p];
+                    if (any) {
+                        seg->T = k.nk > 0 ? k.u1 - k.u0 : 0;
+                        seg->u0 = k.u0;
+                        seg->s = k.s;
+                        seg->g = k.g;
+                        seg->q0 = k.i.q0;
+                        seg->q_len = k.i.q_len;
+                        seg->kv = k.i.kv;
+                        seg->rbase = k.r * RB;
+                        seg->whole = k.whole();
+                        seg->c0 = k.first_cta();
+                        seg->n_ctas = k.last_cta() - seg->c0 + 1;
+                        seg->first = seg->c0 == (int)blockIdx.x;
+                    } else {
+                        seg->T = -1;
+                    }
+                    tc::mbar_arrive(&bar->seg_full[p]);
+                    if (!any) break;
+                    any = k.next(a);
                 }
-                Seg *seg = &bar->seg[p];
-                if (any) {
-                    seg->T = k.nk > 0 ? k.u1 - k.u0 : 0;
-                    seg->u0 = k.u0;
-                    seg->s = k.s;
-                    seg->g = k.g;
-                    seg->q0 = k.i.q0;
-                    seg->q_len = k.i.q_len;
-                    seg->kv = k.i.kv;
-                    seg->rbase = k.r * RB;
-                    seg->whole = k.whole();
-                    seg->first = k.first_cta() == (int)blockIdx.x;
-                } else {
-                    seg->T = -1;
-                }
-                tc::mbar_arrive(&bar->seg_full[p]);
-                if (!any) break;
-                any = k.next(a);
-            }
         }
     } else if (wg <= 2) {
         // -------------------------------------------------------- softmax
@@ -420,14 +572,18 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + gr * TK, to = tmem + lanes + 256 + gr * 128;
         // a negative scale turns the queries' sign, a scale of 0 clears them: c > 0
-        const float c = a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
-        uint32_t sn = 0, on = 0, on1 = 0, met = 0;
+        const float c0 = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e, kLeast);
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+        const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
+        uint32_t sn = 0, on = 0, on1 = 0, met = 0, met1 = 0, tiles = 0;   // phases met, tiles passed
         bool ok = true;
-        auto meet = [&](int which) {                     // both groups (SPLIT)
+        auto meet = [&](int which, uint32_t parity) {    // both groups
             tc::mbar_arrive(&bar->meet[which]);
-            ok = tc::mbar_wait(&bar->meet[which], met & 1, kWaitNs);
+            ok = tc::mbar_wait(&bar->meet[which], parity, kWaitNs);
             return ok;
         };
+        Seg shared[2];                                   // the tiles shared with other CTAs
+        int n_shared = 0;
         for (int sg = 0; ok; ++sg) {
             const Seg *seg = open(sg);
             if (seg == nullptr) {
@@ -437,6 +593,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const int T = seg->T;
             if (T < 0) break;
             int vis;
+            float c = c0;                                // E4: times the row's power of two
             {
                 const int q_len = seg->q_len, kv = seg->kv, rows_all = q_len * a.gqa;
                 const int base = seg->rbase + (PAIR ? gr * TR : 0);
@@ -444,13 +601,12 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (T > 0) {
                     // this group's query rows (SPLIT: its half) into the swizzled layout;
                     // nobody reads the last segment's any more
-                    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-                    const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
                     const int r0 = PAIR ? 0 : gr * (TR / 2), n_rows = PAIR ? TR : TR / 2;
                     uint8_t *dst = qs + (PAIR ? gr * LY::TILE : 0);
                     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                                (int64_t)seg->q0 * a.q_stride +
                                                (int64_t)seg->g * a.gqa * D;
+#pragma unroll 4
                     for (int i = tid & 127; i < n_rows * (D / 8); i += 128) {
                         const int r = r0 + i / (D / 8), c16 = i % (D / 8), qrow = base + r;
                         uint4 v = make_uint4(0, 0, 0, 0);
@@ -463,99 +619,208 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             v.z = (v.z ^ flip) & keep;
                             v.w = (v.w ^ flip) & keep;
                         }
+                        if constexpr (E4) {
+                            // f16, the row's largest entry in [1, 2)
+                            int e = max_exponent(v);
+#pragma unroll
+                            for (int o = 1; o < D / 8; o <<= 1)
+                                e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+                            const float dn = pow2i(-row_exponent(e));
+                            v = make_uint4(f16_of_bf16(v.x, dn), f16_of_bf16(v.y, dn),
+                                           f16_of_bf16(v.z, dn), f16_of_bf16(v.w, dn));
+                        }
                         *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * LY::ATOM + r * 128 +
                                                    (((c16 & 7) ^ (r & 7)) << 4)) = v;
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
+                    if constexpr (E4) {                  // the power of two of this thread's row
+                        const int qrow = base + row;
+                        int e = 0;
+                        if (qrow < rows_all && keep) {
+                            const int t = qrow / a.gqa, h = qrow - t * a.gqa;
+                            const uint4 *p = reinterpret_cast<const uint4 *>(
+                                src + (int64_t)t * a.q_stride + h * D);
+#pragma unroll
+                            for (int i = 0; i < D / 8; ++i) e = max(e, max_exponent(__ldg(p + i)));
+                        }
+                        c *= pow2i(row_exponent(e));
+                    }
                 }
                 vis -= seg->u0 * TK;                     // from the segment's first key
             }
-            float m = -INFINITY, l = 0.f;
+            // m: reference of the weights (log2).  E4: mp, that of the weights times
+            // v_scale, which are what the product with V takes in f16; O is in units
+            // of 2^mp.  Both move when a tile exceeds one of them by kMoveMax.
+            float m = -INFINITY, mp = -INFINITY, l = 0.f;
             constexpr int step = PAIR ? 1 : 2;
-            for (int j = PAIR ? 0 : gr; j < T; j += step) {
-                if (!tc::mbar_wait(&bar->s_full[gr], sn & 1, kWaitNs)) {
-                    ok = false;
-                    break;
+            uint32_t a_col = HK;                         // as the issuer's
+            // pv_done phases are met in turn, each before its half's weights are next
+            // handed over; `early`: already met, to rescale O
+            uint32_t early = 0;
+            for (int j = PAIR ? 0 : gr; j < T && ok; j += step, a_col ^= HK, ++sn) {
+                const bool head = j < step;              // the group's first tile of the segment
+                if constexpr (E4) {
+                    const uint32_t tile = tiles + j;
+                    if (!tc::mbar_wait(&bar->sc_full[tile % kScales], (tile / kScales) & 1, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                ++sn;
-                tc::tc_fence_after();
-                uint32_t s[TK];
-#pragma unroll
-                for (int i = 0; i < TK; i += 32) tc::tmem_ld32_async(ts + i, s + i);
-#pragma unroll
-                for (int i = 0; i < TK; i += 16) tc::tmem_wait_ld(s + i);
-                if (__any_sync(0xffffffffu, (j + 1) * TK > vis)) {
-                    const int seen = vis - j * TK;
-#pragma unroll
-                    for (int i = 0; i < TK; ++i)
-                        if (i >= seen) s[i] = 0xFF800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-                for (int i = 4; i < 124; i += 8)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[i + e], s[i + 4 + e]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[124 + e]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                const float m_new = fmaxf(m, top);
-                const bool grow = m_new > m + kMoveMax || (m == -INFINITY && m_new > m);
-                if (__any_sync(0xffffffffu, grow)) {
-                    // s_full follows every earlier product of this thread's group, so O
-                    // is complete; the first tile's O is overwritten, not added to
-                    const float f = m == -INFINITY ? 0.f : ex2(m - m_new);
-                    l *= f;
-                    if (j >= step) {
 #pragma unroll 1
-                        for (int i = 0; i < D; i += 16) {
-                            uint32_t o[16];
-                            tc::tmem_ld16_async(to + i, o);
-                            tc::tmem_wait_ld(o);
+                for (int h = 0; h < 2; ++h) {
+                    float kc[2], lv[2];                  // factor of a page's scores, log2 v_scale
+                    if constexpr (E4) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc::tmem_st16(to + i, o);
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 sc = bar->scale[(tiles + j) % kScales][2 * h + i];
+                            kc[i] = fmaxf(c * sc.x, kLeast);
+                            lv[i] = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
                         }
                     }
-                    m = m_new;
-                }
-                const float off = m == -INFINITY ? 0.f : -m;
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < TK / 32; ++h) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float2 x = fma2(s[h * 32 + 2 * i], s[h * 32 + 2 * i + 1], c, off);
-                        x.x = ex2(x.x);
-                        x.y = ex2(x.y);
-                        sum[i & 1] = add2(sum[i & 1], x);
-                        p[i] = pack_bf16(x.x, x.y);
+                    if (!tc::mbar_wait(&bar->s_full[gr][h], sn & 1, kWaitNs)) {
+                        ok = false;
+                        break;
                     }
-                    tc::tmem_st16(ts + h * 16, p);
+                    tc::tc_fence_after();
+                    uint32_t s[HK];
+                    const uint32_t sc = ts + (h == 0 ? a_col : a_col ^ HK);
+                    tc::tmem_ld32_async(sc, s);
+                    tc::tmem_ld32_async(sc + 32, s + 32);
+#pragma unroll
+                    for (int i = 0; i < HK; i += 16) tc::tmem_wait_ld(s + i);
+                    if (h == 1) {
+                        tc::tc_fence_before();
+                        tc::mbar_arrive(&bar->sb_free[gr]);
+                    }
+                    const int seen = vis - j * TK - h * HK;
+                    if (__any_sync(0xffffffffu, seen < HK)) {
+#pragma unroll
+                        for (int i = 0; i < HK; ++i)
+                            if (i >= seen) s[i] = 0xFF800000u;
+                    }
+                    // The half is weighed against the m so far while its own maxima are
+                    // taken (the exponentials leave issue slots free); in the rare one that
+                    // exceeds m by kMoveMax, m moves and the half is weighed again.
+                    bool settled = false;
+                    const bool fresh = __any_sync(0xffffffffu, m == -INFINITY);
+                    float sum = 0.f;
+                    for (;;) {
+                        if (!fresh || settled) {
+                            const float off = m == -INFINITY ? 0.f : -m;
+                            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                // E4: from weights to what multiplies V's codes
+                                const float w = E4 && m != -INFINITY ? ex2(lv[y] + m - mp) : 0.f;
+                                uint32_t p[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float2 x = fma2(s[y * 32 + 2 * i], s[y * 32 + 2 * i + 1], E4 ? kc[y] : c,
+                                                    off);
+                                    x.x = ex2(x.x);
+                                    x.y = ex2(x.y);
+                                    part[i & 1] = add2(part[i & 1], x);
+                                    if constexpr (E4) {
+                                        x = mul2(x, w);
+                                        p[i] = pack_f16(x.x, x.y);
+                                    } else {
+                                        p[i] = pack_bf16(x.x, x.y);
+                                    }
+                                }
+                                tc::tmem_st16(ts + a_col + h * 32 + y * 16, p);
+                            }
+                            sum = (part[0].x + part[0].y) + (part[1].x + part[1].y);
+                        }
+                        if (settled) break;
+                        float mx[8];                     // four of each page
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mx[e] = max3(__uint_as_float(s[e * 8]), s[e * 8 + 1], s[e * 8 + 2]);
+#pragma unroll
+                        for (int i = 3; i < 7; i += 2)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) mx[e] = max3(mx[e], s[e * 8 + i], s[e * 8 + i + 1]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(s[e * 8 + 7]));
+                        const float top0 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        const float top1 = fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                        float m_new, mp_new;
+                        bool grow;
+                        if constexpr (E4) {
+                            const float x0 = top0 * kc[0], x1 = top1 * kc[1];
+                            m_new = fmaxf(m, fmaxf(x0, x1));
+                            mp_new = fmaxf(mp, fmaxf(x0 + lv[0], x1 + lv[1]));
+                            grow = m_new > m + kMoveMax || mp_new > mp + kMoveMax;
+                        } else {
+                            m_new = mp_new = fmaxf(m, fmaxf(top0, top1) * c);
+                            grow = m_new > m + kMoveMax;
+                        }
+                        if (!fresh && !__any_sync(0xffffffffu, grow)) break;
+                        const bool none = m == -INFINITY;
+                        l *= none ? 0.f : ex2(m - m_new);
+                        if (!head || h == 1) {
+                            // O has to hold the products so far: those of the half before are
+                            // not implied by these scores (the first half's of a tile: both
+                            // of the last tile's).  The first product overwrites O.
+                            if (h == 0) {
+                                if (!(early & 1) && !tc::mbar_wait(&bar->pv_done[gr][0], (sn - 1) & 1, kWaitNs))
+                                    ok = false;
+                                if (!tc::mbar_wait(&bar->pv_done[gr][1], (sn - 1) & 1, kWaitNs)) ok = false;
+                                early = 3;
+                            } else {
+                                if (!tc::mbar_wait(&bar->pv_done[gr][0], sn & 1, kWaitNs)) ok = false;
+                                early |= 4;
+                            }
+                            tc::tc_fence_after();
+                            const float f = none ? 0.f : ex2(mp - mp_new);
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                uint32_t o[16];
+                                tc::tmem_ld16_async(to + i, o);
+                                tc::tmem_wait_ld(o);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::tmem_st16(to + i, o);
+                            }
+                        }
+                        m = m_new;
+                        mp = mp_new;
+                        settled = true;
+                    }
+                    l += sum;
+                    if (!head && !(early >> h & 1) &&
+                        !tc::mbar_wait(&bar->pv_done[gr][h], (sn - 1) & 1, kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&bar->p_full[gr][h]);
                 }
-                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bar->p_full[gr]);
+                early >>= 2;
             }
             if (!ok) break;
+            tiles += T;
             // ------------------------------------------------ the segment's end
             const bool mine = T > (PAIR ? 0 : gr);      // this group has an O
             if (mine) {
-                if (!tc::mbar_wait(&bar->o_full[gr], on & 1, kWaitNs)) {
+                if (!tc::mbar_wait(&bar->o_full[gr], on & 1, kWaitNs) ||
+                    !(early & 1 || tc::mbar_wait(&bar->pv_done[gr][0], (sn - 1) & 1, kWaitNs)) ||
+                    !tc::mbar_wait(&bar->pv_done[gr][1], (sn - 1) & 1, kWaitNs)) {
                     ok = false;
                     break;
                 }
                 ++on;
             }
-            float f0 = 1.f, f1 = 0.f;
+            // O to units of 2^m
+            float f0 = E4 && m != -INFINITY ? ex2(mp - m) : 1.f, f1 = 0.f;
             if (!PAIR) {
-                if (gr == 1) ml1[row] = make_float2(m, l);
-                if (!meet(0)) break;
+                if (gr == 1) {
+                    ml1[row] = make_float2(m, l);
+                    if (E4) mp1[row] = f0;
+                }
+                if (!meet(0, met & 1)) break;
                 if (gr == 0) {                          // group 0 writes the rows
                     const float2 o1 = ml1[row];
                     if (T > 1) {
@@ -566,23 +831,24 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ++on1;
                     }
                     const float mm = fmaxf(m, o1.x), base = mm == -INFINITY ? 0.f : mm;
-                    f0 = ex2(m - base);
-                    f1 = ex2(o1.x - base);
-                    l = l * f0 + o1.y * f1;
+                    const float g0 = ex2(m - base), g1 = ex2(o1.x - base);
+                    f0 *= g0;
+                    f1 = E4 ? g1 * mp1[row] : g1;
+                    l = l * g0 + o1.y * g1;
                     m = mm;
                 }
             }
+            const bool whole = seg->whole;
             if (PAIR || gr == 0) {
                 tc::tc_fence_after();
-                const bool whole = seg->whole;
                 const int prow = (PAIR ? gr * TR : 0) + row, qrow = seg->rbase + prow;
                 const bool live = qrow < seg->q_len * a.gqa;
                 const int tok = qrow / a.gqa, h = seg->g * a.gqa + qrow - tok * a.gqa;
                 float *rec = a.part + part_slot(blockIdx.x, seg->first) * ((size_t)RB * (D + 2));
-                const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                     (int64_t)(seg->q0 + tok) * a.out_stride + (int64_t)h * D;
                 if (whole) {
+                    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                    f0 *= inv;
+                    f1 *= inv;
                     if (live && a.lse)
                         a.lse[(int64_t)(seg->q0 + tok) * a.H + h] =
                             m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
@@ -590,6 +856,8 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     rec[(size_t)RB * D + prow] = m;
                     rec[(size_t)RB * (D + 1) + prow] = l;
                 }
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
+                                     (int64_t)(seg->q0 + tok) * a.out_stride + (int64_t)h * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
@@ -597,6 +865,8 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         tc::tmem_ld32_async(to + i, o);
                         tc::tmem_wait_ld(o);
                         tc::tmem_wait_ld(o + 16);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0;
@@ -608,8 +878,8 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         tc::tmem_wait_ld(o1 + 16);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f0 +
-                                                   __uint_as_float(o1[e]) * f1);
+                            o[e] = __float_as_uint(
+                                fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
                     }
                     if (whole) {
                         if (live) {
@@ -617,7 +887,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             for (int e = 0; e < 32; e += 8) {
                                 float v[8];
 #pragma unroll
-                                for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[e + x]) * inv;
+                                for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(o[e + x]);
                                 *reinterpret_cast<uint4 *>(dst + i + e) =
                                     VecTraits<__nv_bfloat16>::pack(v);
                             }
@@ -632,22 +902,56 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 tc::tc_fence_before();
             }
-            // SPLIT: Q and group 1's sums may be overwritten once both are here
-            if (!PAIR) {
-                if (!meet(1)) break;
-                ++met;
+            if (!whole) {
+                // every thread's part is visible before this CTA counts itself
+                __threadfence();
+                shared[n_shared++ & 1] = *seg;
             }
+            // SPLIT: Q and group 1's sums may be overwritten once both are here
+            if (!PAIR || !whole) {
+                if (!meet(1, met1 & 1)) break;
+                ++met1;
+                if (!whole && tid == 128) tc::red_release_gpu_add(a.count + seg->c0, 1);
+            }
+            ++met;
             close(sg);
+        }
+        // ---------------------------------------------------- the shared tiles
+        // Once all of a tile's CTAs have left their part, each joins a share of its
+        // rows, the parts in CTA order.  All CTAs run at the same time (a cooperative
+        // launch), so this waits for no CTA that has yet to start.
+        for (int x = 0; x < n_shared && ok; ++x) {
+            const Seg &sh = shared[x];
+            int *count = a.count + sh.c0, *left = a.count + kAttendMaxCtas + sh.c0;
+            if (tid == 128) {
+                bool all = tc::ld_acquire_gpu(count) >= sh.n_ctas;
+                const uint32_t t0 = tc::global_ns_lo();
+                while (!all && tc::global_ns_lo() - t0 < kWaitNs) all = tc::ld_acquire_gpu(count) >= sh.n_ctas;
+                bar->go = all;
+                if (!all) atomicOr(err, 4);
+            }
+            if (!meet(1, met1++ & 1)) break;
+            const bool all = bar->go != 0;
+            __threadfence();
+            if (all) join_rows<D, RB>(a, sh, blockIdx.x - sh.c0, tid - 128);
+            if (!meet(1, met1++ & 1)) break;             // go and the counters are free
+            if (tid == 128) {
+                // the last CTA to leave readies the counters for the next call
+                __threadfence();
+                if (atomicAdd(left, 1) == sh.n_ctas - 1) {
+                    *count = 0;
+                    *left = 0;
+                }
+            }
         }
         if (!ok) atomicOr(err, 4);
     } else {
-        // -------------------------------------------------------- e4m3 -> bf16
+        // -------------------------------------------------------- e4m3 -> f16
         if constexpr (E4) {
             tc::regs_release<88>();
             const int w = warp & 3;                      // its page of the tile
             int n = 0;                                   // K / V tiles converted
             bool ok = true;
-            const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((120 + 127) << 23));
             for (int sg = 0; ok; ++sg) {
                 const Seg *seg = open(sg);
                 if (!__all_sync(0xffffffffu, seg != nullptr)) {
@@ -658,12 +962,13 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int64_t table = (int64_t)seg->s * a.b.table_stride;
                 close(sg);
                 if (T < 0) break;
-                float ks = 1.f, vs = 1.f;                // lane i: of the page of tile 32 x + i
+                float2 sc_of = make_float2(1.f, 1.f);    // lane i: of the page of tile 32 x + i
                 int rows_of = 0;
                 for (int j = 0; j < T && ok; ++j) {
                     if ((j & 31) == 0) {                 // the scales of 32 tiles at once
                         const int p = (u0 + j + lane) * kPagesPerTile + w;
                         rows_of = 0;
+                        sc_of = make_float2(1.f, 1.f);
                         if (j + lane < T && p * kBlockTokens < kv_len) {
                             const int64_t page = a.b.page_table[table + p];
                             bool there = page >= 0 && page < a.b.n_pages;
@@ -671,8 +976,8 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                 const int64_t r = a.b.scale_rows ? (int64_t)a.b.scale_rows[table + p] : page;
                                 if (r >= 0 && r < a.b.n_scale_rows) {
                                     const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + g;
-                                    ks = checked_scale(a.k_scale[so], err);
-                                    vs = checked_scale(a.v_scale[so], err);
+                                    sc_of = make_float2(checked_scale(a.k_scale[so], err),
+                                                        checked_scale(a.v_scale[so], err));
                                 } else {
                                     atomicOr(err, kErrBatch);
                                     there = false;
@@ -682,48 +987,48 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         }
                     }
                     const int rows = __shfl_sync(0xffffffffu, rows_of, j & 31);
+                    const float2 sc = make_float2(__shfl_sync(0xffffffffu, sc_of.x, j & 31),
+                                                  __shfl_sync(0xffffffffu, sc_of.y, j & 31));
                     for (int kv = 0; kv < 2; ++kv, ++n) {
                         const int rs = n % NR, s = n % NS;
-                        const __nv_bfloat162 scale = __float2bfloat162_rn(
-                            __shfl_sync(0xffffffffu, kv ? vs : ks, j & 31));
                         if (!__all_sync(0xffffffffu,
                                         tc::mbar_wait(&bar->raw_full[rs], (n / NR) & 1, kWaitNs) &&
                                             tc::mbar_wait(&bar->empty[s], ((n / NS) & 1) ^ 1, kWaitNs))) {
                             ok = false;
                             break;
                         }
+                        if (kv == 0 && lane == 0) {
+                            // K's slot was V's of the tile before the last, which both groups
+                            // are done with: the place of four tiles ago is free
+                            const int x = (n >> 1) % kScales;
+                            bar->scale[x][w] = sc;
+                            tc::mbar_arrive(&bar->sc_full[x]);
+                        }
                         const uint8_t *src = raws + rs * LY::RAW + w * kBlockTokens * D;
                         uint8_t *dst = kvs + s * LY::TILE;
                         constexpr int CPR = D / 16;      // 16-byte pieces of a raw row
+                        constexpr int N = kBlockTokens * CPR / 32;
+                        uint4 in[N];
 #pragma unroll
-                        for (int i = lane; i < kBlockTokens * CPR; i += 32) {
-                            const int r = i / CPR, c = i % CPR, key = w * kBlockTokens + r;
-                            uint4 x = *reinterpret_cast<const uint4 *>(src + i * 16);
-                            if (r >= rows) x = make_uint4(0, 0, 0, 0);
-                            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                            uint32_t out[8], nan = 0;
+                        for (int i = 0; i < N; ++i)
+                            in[i] = *reinterpret_cast<const uint4 *>(src + (i * 32 + lane) * 16);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                out[2 * e] = e4m3_bf16(__byte_perm(in[e], 0, 0x1404), up, scale);
-                                out[2 * e + 1] = e4m3_bf16(__byte_perm(in[e], 0, 0x3424), up, scale);
-                                nan |= (in[e] & 0x7F7F7F7Fu) + 0x01010101u;
-                            }
-                            if (nan & 0x80808080u) {     // a NaN code: S.1111.111
-#pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if ((in[e >> 2] >> (8 * (e & 3)) & 0x7F) == 0x7F)
-                                        out[e >> 1] |= 0x7FC0u << (16 * (e & 1));
-                            }
-                            // the two 16-byte chunks of the row's atom; the lanes of the
-                            // second atom write theirs in the other order (bank conflicts)
+                        for (int i = 0; i < N; ++i) {
+                            const int at = i * 32 + lane, r = at / CPR, c = at % CPR;
+                            const int key = w * kBlockTokens + r;
+                            if (r >= rows) in[i] = make_uint4(0, 0, 0, 0);
+                            const uint4 lo = make_uint4(e4m3_f16(in[i].x), e4m3_f16(in[i].x >> 16),
+                                                        e4m3_f16(in[i].y), e4m3_f16(in[i].y >> 16));
+                            const uint4 hi = make_uint4(e4m3_f16(in[i].z), e4m3_f16(in[i].z >> 16),
+                                                        e4m3_f16(in[i].w), e4m3_f16(in[i].w >> 16));
+                            // two 16-byte chunks of the row's atom; the lanes of the second
+                            // atom write theirs in the other order (bank conflicts)
                             uint8_t *row = dst + (c >> 2) * LY::ATOM + key * 128;
                             const int c0 = (c & 3) * 2, odd = (c >> 2) & 1;
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int h = e ^ odd;
-                                *reinterpret_cast<uint4 *>(row + (((c0 + h) ^ (key & 7)) << 4)) =
-                                    h ? make_uint4(out[4], out[5], out[6], out[7])
-                                      : make_uint4(out[0], out[1], out[2], out[3]);
+                                *reinterpret_cast<uint4 *>(row + (((c0 + h) ^ (key & 7)) << 4)) = h ? hi : lo;
                             }
                         }
                         tc::fence_proxy_async_smem();
@@ -741,70 +1046,6 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tc::tc_fence_after();
         tc::tmem_dealloc(tmem, 512);
     }
-}
-
-// Joins the partial sums of the row tiles that several CTAs share: block
-// (c, y) takes the tile that begins in CTA c and goes on, rows y, y + ...  The
-// work line is laid out as in the kernel before.
-template <int D, bool PAIR>
-__global__ void __launch_bounds__(256)
-attend_join_kernel(const __grid_constant__ AttendArgs a, int n_ctas, int min_units) {
-    constexpr int RB = PAIR ? 2 * TR : TR;
-    constexpr int ROWS = 32;                             // rows of a block
-    constexpr size_t REC = (size_t)RB * (D + 2);
-    __shared__ int64_t pre[kMaxSeqs + 1];
-    using W = Walk<RB, TK>;
-    const int c = blockIdx.x;
-    W::LN::lay_out(a, pre);
-    const int64_t total = pre[a.b.n_seqs];
-    const int64_t per = max((int64_t)min_units, (total + n_ctas - 1) / n_ctas);
-    const int64_t end = min(total, (c + 1) * per);
-    // every block waits for the kernel before: the stream's next one must not
-    // begin while it runs
-    tc::wait_prior_grids();
-    if (c * per >= end) return;
-    // the tile of the run's last unit
-    W k;
-    k.start_at(a, pre, end - 1, per);
-    const int64_t x0 = k.x - k.u0;
-    if (x0 < c * per || x0 + k.w <= end) return;         // begun earlier, or complete
-    const int c1 = (int)((x0 + k.w - 1) / per);
-    const int row = blockIdx.y * ROWS + (threadIdx.x & 31);
-    const int qrow = k.r * RB + row;
-    if (qrow >= k.i.q_len * a.gqa) return;
-    float m = -INFINITY;
-    for (int p = c; p <= c1; ++p)
-        m = fmaxf(m, __ldcg(a.part + part_slot(p, p == c) * REC + (size_t)RB * D + row));
-    const float base = m == -INFINITY ? 0.f : m;
-    constexpr int PER = D / 4 / 8;                       // column quads of a thread
-    float4 o[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    const int q0 = threadIdx.x >> 5;
-    for (int p = c; p <= c1; ++p) {
-        const float *rec = a.part + part_slot(p, p == c) * REC;
-        const float f = ex2(__ldcg(rec + (size_t)RB * D + row) - base);
-        l += f * __ldcg(rec + (size_t)RB * (D + 1) + row);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(rec) + (size_t)(q0 + 8 * i) * RB + row);
-            o[i].x += f * v.x;
-            o[i].y += f * v.y;
-            o[i].z += f * v.z;
-            o[i].w += f * v.w;
-        }
-    }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int tok = qrow / a.gqa, h = k.g * a.gqa + qrow - tok * a.gqa;
-    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(k.i.q0 + tok) * a.out_stride +
-                         (int64_t)h * D;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        *reinterpret_cast<uint2 *>(dst + (q0 + 8 * i) * 4) =
-            make_uint2(pack_bf16(o[i].x * inv, o[i].y * inv), pack_bf16(o[i].z * inv, o[i].w * inv));
-    if (a.lse && q0 == 0)
-        a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
 }
 
 // ---------------------------------------------------------------- host side
@@ -839,7 +1080,7 @@ bool page_map(CUtensorMap *m, const void *pages, int d, int64_t heads) {
 
 template <int D, bool E4, bool PAIR>
 cudaError_t tile_t(const AttendArgs &a, cudaStream_t s) {
-    using LY = Lay<D, E4>;
+    using LY = Lay<D, E4, PAIR>;
     CUtensorMap kmap{}, vmap{};
     if (!E4) {
         const int64_t heads = a.b.n_pages * a.b.L * a.b.G;
@@ -850,20 +1091,12 @@ cudaError_t tile_t(const AttendArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = min(kTileMaxCtas, sm_count());
-    const int min_units = PAIR ? 2 : 4;
-    kern<<<ctas, LY::THREADS, LY::SMEM, s>>>(kmap, vmap, a, min_units);
-    note_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, PAIR ? 8 : 4);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_join_kernel<D, PAIR>, a, ctas, min_units);
+    int min_units = kMinTiles;
+    AttendArgs args = a;
+    void *params[] = {&kmap, &vmap, &args, &min_units};
+    // CTAs that share a tile wait for one another at the end: all run at once
+    e = cudaLaunchCooperativeKernel((const void *)kern, dim3((unsigned)ctas), dim3(LY::THREADS), params,
+                                    LY::SMEM, s);
     note_launch();
     return e;
 }

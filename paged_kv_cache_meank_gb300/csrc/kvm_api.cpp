@@ -159,7 +159,7 @@ Layout layout_of(const kvm_config *c) {
                      (size_t)(kStatSlots + 1) * 8 + 1) *
                     sizeof(int32_t));
     lo.attend = take(kvm::attend_scratch_bytes());
-    lo.attend_count = take(kvm::kAttendMaxCtas * sizeof(int));
+    lo.attend_count = take(2 * kvm::kAttendMaxCtas * sizeof(int));
     lo.err = take(256);
     lo.total = off;
     return lo;
@@ -460,7 +460,7 @@ kvm_status kvm_create(const kvm_config *cfg, void *workspace, size_t workspace_b
     if ((e = kvm::launch_rope_table(c->table, cfg->max_positions, hd, om, s)) != cudaSuccess)
         return cleanup(cuda_fail(e, "rope table"));
     if ((e = cudaMemsetAsync(c->err_dev, 0, sizeof(int), s)) != cudaSuccess ||
-        (e = cudaMemsetAsync(c->ws + lo.attend_count, 0, kvm::kAttendMaxCtas * sizeof(int), s)) !=
+        (e = cudaMemsetAsync(c->ws + lo.attend_count, 0, 2 * kvm::kAttendMaxCtas * sizeof(int), s)) !=
             cudaSuccess)
         return cleanup(cuda_fail(e, "cudaMemsetAsync"));
     if (c->device_diff) {
@@ -1187,6 +1187,10 @@ kvm_status kvm_sync(kvm_ctx *c, kvm_stream stream) {
     KVM_CUDA(cudaMemcpy(&flag, c->err_dev, sizeof(int), cudaMemcpyDeviceToHost));
     if (flag) {
         KVM_CUDA(cudaMemset(c->err_dev, 0, sizeof(int)));
+        // an attention call that gave up may have left its arrival counts
+        if (flag & 4)
+            KVM_CUDA(cudaMemset(c->ws + c->lo.attend_count, 0,
+                                2 * kvm::kAttendMaxCtas * sizeof(int)));
         if (flag & 4) return fail(KVM_ERR_TIMEOUT, "a bounded device wait gave up (flag 0x%x)", flag);
         return fail(KVM_ERR_DEVICE, "device range check raised flag 0x%x", flag);
     }

@@ -32,7 +32,7 @@ struct CtxView {
     const float2 *table;   // cos/sin, [max_positions][d / 2]
     int *err;              // device error flag
     float *attend_part;    // kvm_attend: partial outputs of split rows
-    int *attend_count;     // kvm_attend: arrivals per CTA, zero between calls
+    int *attend_count;     // kvm_attend: arrivals and departures per CTA
     int device;
 };
 CtxView ctx_view(const kvm_ctx *c);
@@ -266,7 +266,7 @@ struct AttendArgs {
     int64_t out_stride;
     float *lse;
     float *part;                   // partial outputs (attend_scratch_bytes)
-    int *count;                    // arrivals, [kAttendMaxCtas]
+    int *count;                    // arrivals, departures: [2][kAttendMaxCtas], zero between calls
 };
 constexpr int kAttendMaxCtas = 608;    // CTAs of one attention grid, at most
 size_t attend_scratch_bytes();         // of AttendArgs::part
