@@ -32,7 +32,7 @@ struct Lay {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = RB * D;
     static constexpr int FLOATS = OFF_P + NBUF * PAGE;
-    static constexpr int SMEM = FLOATS * 4 + (kMaxSeqs + 2) * 8;
+    static constexpr int SMEM = FLOATS * 4 + (kMaxSeqs + 3) * 8;
 };
 
 }  // namespace
@@ -49,7 +49,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
     __shared__ int is_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::lay_out(a, pre);
+    if (warp == 0) W::LN::template lay_out<false>(a, pre);
     __syncthreads();
     W k;
     if (!k.start(a, pre, cta, gridDim.x, min_units)) return;

@@ -47,11 +47,36 @@ struct Line {
     __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, int gqa, int causal, int r) {
         return max(1, (keys(i, gqa, causal, r) + UNIT - 1) / UNIT);
     }
-    // pre[s] = units of the sequences before s, pre[n_seqs] = all, pre[n_seqs + 1]
-    // = the largest tile's (pre: kMaxSeqs + 2 in shared memory).  By one warp.
+    // A sequence's units by one head, as summed by the lane (few row tiles) or the
+    // warp; every lane of the warp calls it with its sequence's lengths.
+    __device__ static int64_t units(const SeqInfo &i, int gqa, int causal, int n_here, int lane) {
+        const int n = tiles(i, gqa);
+        int64_t w = 0;
+        if (__all_sync(0xffffffffu, n <= 8)) {
+            for (int r = 0; r < n; ++r) w += weight(i, gqa, causal, r);
+            return w;
+        }
+        for (int x = 0; x < n_here; ++x) {
+            SeqInfo j;
+            j.q0 = 0;
+            j.q_len = __shfl_sync(0xffffffffu, i.q_len, x);
+            j.kv = __shfl_sync(0xffffffffu, i.kv, x);
+            const int m = tiles(j, gqa);
+            int64_t sum = 0;
+            for (int r = lane; r < m; r += 32) sum += weight(j, gqa, causal, r);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == x) w = sum;
+        }
+        return w;
+    }
+    // Lays the line out: pre[s] = units of the sequences before s, pre[n_seqs] =
+    // all, pre[n_seqs + 1] = the largest tile's, pre[n_seqs + 2] = the units every
+    // tile is counted as, or 0 for its own (see run_units).  By one warp.
+    template <bool PAD>
     __device__ static void lay_out(const AttendArgs &a, int64_t *pre) {
         const int lane = threadIdx.x & 31;
-        int64_t run = 0;
+        int64_t run = 0, items = 0;
         int most = 1;
         for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
             const int s = s0 + lane;
@@ -60,42 +85,57 @@ struct Line {
             if (s < a.b.n_seqs) i = seq_info(a.b, s, &ok);
             if (!ok) atomicOr(a.b.err, kErrBatch);
             const int n = tiles(i, a.gqa);
-            int64_t w = 0;
-            // few tiles each: a lane sums its sequence's; many: the warp takes the
-            // sequences in turn
-            if (__all_sync(0xffffffffu, n <= 8)) {
-                for (int r = 0; r < n; ++r) w += weight(i, a.gqa, a.causal, r);
-            } else {
-                for (int x = 0; x < min(32, a.b.n_seqs - s0); ++x) {
-                    SeqInfo j;
-                    j.q0 = 0;
-                    j.q_len = __shfl_sync(0xffffffffu, i.q_len, x);
-                    j.kv = __shfl_sync(0xffffffffu, i.kv, x);
-                    const int m = tiles(j, a.gqa);
-                    int64_t sum = 0;
-                    for (int r = lane; r < m; r += 32) sum += weight(j, a.gqa, a.causal, r);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == x) w = sum;
-                }
-            }
             if (n > 0) most = max(most, weight(i, a.gqa, a.causal, n - 1));   // the last sees most
-            w *= a.b.G;
+            int64_t w = units(i, a.gqa, a.causal, min(32, a.b.n_seqs - s0), lane) * a.b.G;
+            int64_t m = (int64_t)n * a.b.G;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
-                if (lane >= o) w += up;
+                const int64_t um = __shfl_up_sync(0xffffffffu, m, o);
+                if (lane >= o) {
+                    w += up;
+                    m += um;
+                }
             }
             if (s < a.b.n_seqs) pre[s + 1] = run + w;
             run += __shfl_sync(0xffffffffu, w, 31);
+            items += __shfl_sync(0xffffffffu, m, 31);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        int pad = 0;
+        if (PAD) pad = padded_weight(items, run, most, a);
+        if (pad) {
+            // every tile counts alike: the prefix sums again, by tiles
+            run = 0;
+            for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
+                const int s = s0 + lane;
+                bool ok;
+                int64_t w = s < a.b.n_seqs ? (int64_t)tiles(seq_info(a.b, s, &ok), a.gqa) * a.b.G * pad : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
+                    if (lane >= o) w += up;
+                }
+                if (s < a.b.n_seqs) pre[s + 1] = run + w;
+                run += __shfl_sync(0xffffffffu, w, 31);
+            }
+        }
         if (lane == 0) {
             pre[0] = 0;
             pre[a.b.n_seqs + 1] = most;
+            pre[a.b.n_seqs + 2] = pad;
         }
         __syncwarp();
+    }
+    // Row tiles of one head read the same keys.  CTAs that begin theirs at scattered
+    // keys fetch the cache once each (762 MB of a 134 MB cache were read); where the
+    // tiles are about equally long, counting them all as the longest (a multiple of
+    // 12) lets runs begin at the same few places.
+    __host__ __device__ static int padded_weight(int64_t items, int64_t total, int most, const AttendArgs &a) {
+        const bool shared = (int64_t)a.b.max_q_len * a.gqa > RB;   // tiles that read the same keys
+        const int pad = (most + 11) / 12 * 12;
+        return shared && most >= 24 && total * 100 >= items * pad * 85 ? pad : 0;
     }
 };
 
@@ -107,11 +147,28 @@ __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // Units of one CTA's run: an equal share, but not so small that a tile's join
-// costs more than its keys, unless whole tiles are smaller.
+// costs more than its keys, unless whole tiles are smaller.  With equal tiles, a
+// multiple of a tile's whole, half, third or quarter: the first of them that
+// gives away at most 1/16 of the share, else the one that gives away least.
 __host__ __device__ __forceinline__ int64_t run_units(const AttendArgs &a, const int64_t *pre, int n_ctas,
                                                       int min_units) {
     const int64_t share = quotient(pre[a.b.n_seqs] + n_ctas - 1, n_ctas);
     const int64_t most = pre[a.b.n_seqs + 1], least = most < min_units ? most : min_units;
+    const int64_t pad = pre[a.b.n_seqs + 2];
+    if (pad && share * 4 > pad) {
+        int64_t best = 0;
+        for (int m = 1; m <= 4; ++m) {
+            const int64_t part = pad / m, run = quotient(share + part - 1, part) * part;
+            if (best == 0 || run < best) best = run;
+            if (run * 16 <= share * 17) return run;
+        }
+        return best;
+    }
+    if (pad) {                                           // a tile in equal parts
+        const int64_t parts = quotient(pad, share);
+        const int64_t run = quotient(pad + parts - 1, parts);
+        return run > least ? run : least;
+    }
     return share > least ? share : least;
 }
 
@@ -121,7 +178,7 @@ struct Walk {
     using LN = Line<RB, UNIT>;
     int64_t x, end, per;     // position, end of the run, units of a run
     int s, g, r, n_tiles;    // sequence, kv head, row tile
-    int u0, u1, w;           // the segment's units [u0, u1) of the tile's w
+    int u0, u1, w, pad;      // the segment's units [u0, u1) of the tile's w (pad: as counted)
     int nk;                  // keys the tile sees
     SeqInfo i;
 
@@ -148,6 +205,7 @@ struct Walk {
             if (pre[m] <= x) lo = m; else hi = m - 1;
         }
         s = lo;
+        pad = (int)pre[a.b.n_seqs + 2];
         bool ok;
         i = seq_info(a.b, s, &ok);
         n_tiles = LN::tiles(i, a.gqa);
@@ -156,9 +214,15 @@ struct Walk {
         g = (int)quotient(rem, per_head);
         rem -= g * per_head;
         r = 0;
-        for (w = LN::weight(i, a.gqa, a.causal, 0); rem >= w; w = LN::weight(i, a.gqa, a.causal, r)) {
-            rem -= w;
-            ++r;
+        if (pad) {
+            r = (int)quotient(rem, pad);
+            rem -= (int64_t)r * pad;
+            w = pad;
+        } else {
+            for (w = LN::weight(i, a.gqa, a.causal, 0); rem >= w; w = LN::weight(i, a.gqa, a.causal, r)) {
+                rem -= w;
+                ++r;
+            }
         }
         u0 = (int)rem;
         fill(a);
@@ -182,9 +246,14 @@ struct Walk {
                 } while (n_tiles == 0);
             }
         }
-        w = LN::weight(i, a.gqa, a.causal, r);
+        w = pad ? pad : LN::weight(i, a.gqa, a.causal, r);
         fill(a);
         return true;
+    }
+    // Key tiles of the segment: its units that hold keys.
+    __host__ __device__ __forceinline__ int key_units() const {
+        const int real = (nk + UNIT - 1) / UNIT;
+        return (u1 < real ? u1 : real) - (u0 < real ? u0 : real);
     }
     __host__ __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == w; }
     // The first and last CTA that share the segment's tile.

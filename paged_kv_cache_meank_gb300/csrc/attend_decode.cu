@@ -46,7 +46,7 @@ struct Lay {
     static constexpr int ORS = D + 4;                      // a row of a warp's joined output
     static constexpr int REC = RB * ORS + 2 * RB;          // floats: o, m, l
     static constexpr int BYTES = WARPS * (RING > REC * 4 ? RING : REC * 4);
-    static constexpr int SMEM = BYTES + (kMaxSeqs + 2) * 8;
+    static constexpr int SMEM = BYTES + (kMaxSeqs + 3) * 8;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -122,7 +122,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::lay_out(a, pre);
+    if (warp == 0) W::LN::template lay_out<false>(a, pre);
     __syncthreads();
     W k;
     if (!k.start(a, pre, cta, gridDim.x, min_units)) return;

@@ -73,7 +73,7 @@ struct Lay {
     static constexpr int OFF_BAR = OFF_ML + (PAIR ? 0 : TR * 12);
     static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
-    static_assert(SLOTS * TILE >= (kMaxSeqs + 2) * 8, "prefix fits the ring");
+    static_assert(SLOTS * TILE >= (kMaxSeqs + 3) * 8, "prefix fits the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -531,7 +531,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             using W = Walk<RB, TK>;
             // the prefix sums live in the ring: its first copies follow the first segment
             int64_t *pre = reinterpret_cast<int64_t *>(kvs);
-            W::LN::lay_out(a, pre);
+            W::LN::template lay_out<PAIR>(a, pre);
             W k;
             bool any = k.start(a, pre, blockIdx.x, gridDim.x, min_units);
             tc::fence_proxy_async_smem();
@@ -545,7 +545,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     }
                     Seg *seg = &bar->seg[p];
                     if (any) {
-                        seg->T = k.nk > 0 ? k.u1 - k.u0 : 0;
+                        seg->T = k.key_units();
                         seg->u0 = k.u0;
                         seg->s = k.s;
                         seg->g = k.g;
