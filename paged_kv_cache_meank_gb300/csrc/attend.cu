@@ -49,7 +49,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
     __shared__ int is_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::template lay_out<false>(a, pre);
+    if (warp == 0) W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
     __syncthreads();
     W k;
     if (!k.start(a, pre, cta, gridDim.x, min_units)) return;

@@ -74,7 +74,7 @@ struct Line {
     // all, pre[n_seqs + 1] = the largest tile's, pre[n_seqs + 2] = the units every
     // tile is counted as, or 0 for its own (see run_units).  By one warp.
     template <bool PAD>
-    __device__ static void lay_out(const AttendArgs &a, int64_t *pre) {
+    __device__ static void lay_out(const AttendArgs &a, int64_t *pre, int n_ctas, int min_units) {
         const int lane = threadIdx.x & 31;
         int64_t run = 0, items = 0;
         int most = 1;
@@ -104,7 +104,7 @@ struct Line {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
         int pad = 0;
-        if (PAD) pad = padded_weight(items, run, most, a);
+        if (PAD) pad = padded_weight(items, run, most, n_ctas, min_units);
         if (pad) {
             // every tile counts alike: the prefix sums again, by tiles
             run = 0;
@@ -128,14 +128,22 @@ struct Line {
         }
         __syncwarp();
     }
-    // Row tiles of one head read the same keys.  CTAs that begin theirs at scattered
-    // keys fetch the cache once each (762 MB of a 134 MB cache were read); where the
-    // tiles are about equally long, counting them all as the longest (a multiple of
-    // 12) lets runs begin at the same few places.
-    __host__ __device__ static int padded_weight(int64_t items, int64_t total, int most, const AttendArgs &a) {
-        const bool shared = (int64_t)a.b.max_q_len * a.gqa > RB;   // tiles that read the same keys
+    // Where the row tiles are about equally long, they are all counted as `pad`
+    // units, at least the longest one's: runs then begin and end at the same few
+    // places of every tile (run_units).  A CTA meets one tile and not the ends of
+    // two, and CTAs that share a head's keys read them at the same time (begun at
+    // scattered keys they read 762 MB of a 134 MB cache).
+    __host__ __device__ static int padded_weight(int64_t items, int64_t total, int most, int n_ctas,
+                                                 int min_units) {
+        if (items == 0 || total * 100 < items * most * 85) return 0;
+        if (items * 4 < (int64_t)n_ctas * 3) {           // several CTAs to a tile
+            const int least = most < min_units ? most : min_units;
+            int parts = (int)(n_ctas / items);
+            if (parts > most / least) parts = most / least;
+            return (most + parts - 1) / parts * parts;
+        }
         const int pad = (most + 11) / 12 * 12;
-        return shared && most >= 24 && total * 100 >= items * pad * 85 ? pad : 0;
+        return most >= 24 && total * 100 >= items * pad * 85 ? pad : 0;
     }
 };
 
@@ -147,29 +155,29 @@ __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 
 // Units of one CTA's run: an equal share, but not so small that a tile's join
-// costs more than its keys, unless whole tiles are smaller.  With equal tiles, a
-// multiple of a tile's whole, half, third or quarter: the first of them that
+// costs more than its keys, unless whole tiles are smaller.  Of tiles counted
+// alike, a CTA takes an equal part of one, or with more tiles than CTAs a
+// multiple of a whole, a half, a third or a quarter: the first of these that
 // gives away at most 1/16 of the share, else the one that gives away least.
 __host__ __device__ __forceinline__ int64_t run_units(const AttendArgs &a, const int64_t *pre, int n_ctas,
                                                       int min_units) {
     const int64_t share = quotient(pre[a.b.n_seqs] + n_ctas - 1, n_ctas);
     const int64_t most = pre[a.b.n_seqs + 1], least = most < min_units ? most : min_units;
     const int64_t pad = pre[a.b.n_seqs + 2];
-    if (pad && share * 4 > pad) {
-        int64_t best = 0;
-        for (int m = 1; m <= 4; ++m) {
-            const int64_t part = pad / m, run = quotient(share + part - 1, part) * part;
-            if (best == 0 || run < best) best = run;
-            if (run * 16 <= share * 17) return run;
-        }
-        return best;
+    if (!pad) return share > least ? share : least;
+    const int64_t items = quotient(pre[a.b.n_seqs], pad);
+    if (items * 4 < (int64_t)n_ctas * 3) {
+        int64_t parts = quotient(n_ctas, items);
+        if (parts > quotient(most, least)) parts = quotient(most, least);
+        return quotient(pad, parts);
     }
-    if (pad) {                                           // a tile in equal parts
-        const int64_t parts = quotient(pad, share);
-        const int64_t run = quotient(pad + parts - 1, parts);
-        return run > least ? run : least;
+    int64_t best = 0;
+    for (int m = 1; m <= 4; ++m) {
+        const int64_t part = pad / m, run = quotient(share + part - 1, part) * part;
+        if (best == 0 || run < best) best = run;
+        if (run * 16 <= share * 17) return run;
     }
-    return share > least ? share : least;
+    return best;
 }
 
 // A walk over one CTA's run of the line.

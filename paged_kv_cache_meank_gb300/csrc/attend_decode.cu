@@ -122,7 +122,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::template lay_out<false>(a, pre);
+    if (warp == 0) W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
     __syncthreads();
     W k;
     if (!k.start(a, pre, cta, gridDim.x, min_units)) return;

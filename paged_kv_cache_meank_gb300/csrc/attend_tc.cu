@@ -70,7 +70,8 @@ struct Lay {
     static constexpr int OFF_KV = Q_TILES * TILE;
     static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE;
     static constexpr int OFF_ML = OFF_RAW + RAW_SLOTS * RAW;       // SPLIT: group 1's sums
-    static constexpr int OFF_BAR = OFF_ML + (PAIR ? 0 : TR * 12);
+    static constexpr int OFF_QP = OFF_ML + (PAIR ? 0 : TR * 12);   // e4m3: the rows' powers of two
+    static constexpr int OFF_BAR = OFF_QP + (E4 ? Q_TILES * TR * 4 : 0);
     static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
     static_assert(SLOTS * TILE >= (kMaxSeqs + 3) * 8, "prefix fits the ring");
@@ -244,9 +245,9 @@ __device__ __forceinline__ void join_rows(const AttendArgs &a, const Seg &sh, in
     const int rows = min(RB, sh.q_len * a.gqa - sh.rbase), n = sh.n_ctas;
     const int r0 = rows * part / n, nr = rows * (part + 1) / n - r0;
     if (n <= 4)
-        for (int x = t; x < nr * (D / 4); x += 256 * 4) join_quads<D, RB, 4, 2>(a, sh, r0, nr, x);
+        for (int x = t; x < nr * (D / 4); x += 256 * 4) join_quads<D, RB, 4, 4>(a, sh, r0, nr, x);
     else
-        for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 5>(a, sh, r0, nr, x);
+        for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 10>(a, sh, r0, nr, x);
 }
 
 }  // namespace
@@ -266,7 +267,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *qs = smem + LY::OFF_Q, *kvs = smem + LY::OFF_KV, *raws = smem + LY::OFF_RAW;
     float2 *ml1 = reinterpret_cast<float2 *>(smem + LY::OFF_ML);
-    float *mp1 = reinterpret_cast<float *>(ml1 + TR);
+    float *mp1 = reinterpret_cast<float *>(ml1 + TR), *qpow = reinterpret_cast<float *>(smem + LY::OFF_QP);
     Bars *bar = reinterpret_cast<Bars *>(smem + LY::OFF_BAR);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
@@ -531,7 +532,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             using W = Walk<RB, TK>;
             // the prefix sums live in the ring: its first copies follow the first segment
             int64_t *pre = reinterpret_cast<int64_t *>(kvs);
-            W::LN::template lay_out<PAIR>(a, pre);
+            W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
             W k;
             bool any = k.start(a, pre, blockIdx.x, gridDim.x, min_units);
             tc::fence_proxy_async_smem();
@@ -575,7 +576,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const float c0 = a.scale == 0.f ? 1.f : fmaxf(fabsf(a.scale) * kLog2e, kLeast);
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
         const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
-        uint32_t sn = 0, on = 0, on1 = 0, met = 0, met1 = 0, tiles = 0;   // phases met, tiles passed
+        uint32_t sn = 0, on = 0, on1 = 0, met = 0, met1 = 0, qn = 0, tiles = 0;   // phases met, tiles passed
         bool ok = true;
         auto meet = [&](int which, uint32_t parity) {    // both groups
             tc::mbar_arrive(&bar->meet[which]);
@@ -601,51 +602,54 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (T > 0) {
                     // this group's query rows (SPLIT: its half) into the swizzled layout;
                     // nobody reads the last segment's any more
-                    const int r0 = PAIR ? 0 : gr * (TR / 2), n_rows = PAIR ? TR : TR / 2;
+                    const int r0 = PAIR ? 0 : gr * (TR / 2);
                     uint8_t *dst = qs + (PAIR ? gr * LY::TILE : 0);
                     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                                (int64_t)seg->q0 * a.q_stride +
                                                (int64_t)seg->g * a.gqa * D;
-#pragma unroll 4
-                    for (int i = tid & 127; i < n_rows * (D / 8); i += 128) {
-                        const int r = r0 + i / (D / 8), c16 = i % (D / 8), qrow = base + r;
-                        uint4 v = make_uint4(0, 0, 0, 0);
+                    constexpr int CPR = D / 8, RPP = 128 / CPR;       // chunks of a row, rows of a pass
+                    constexpr int N = (PAIR ? TR : TR / 2) / RPP;     // a thread's chunks
+                    const int c16 = (tid & 127) % CPR, rr = r0 + (tid & 127) / CPR;
+                    uint4 v[N];                          // all loads in flight together
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int qrow = base + rr + i * RPP;
+                        v[i] = make_uint4(0, 0, 0, 0);
                         if (qrow < rows_all) {
                             const int t = qrow / a.gqa, h = qrow - t * a.gqa;
-                            v = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)t * a.q_stride +
-                                                                      h * D + c16 * 8));
-                            v.x = (v.x ^ flip) & keep;
-                            v.y = (v.y ^ flip) & keep;
-                            v.z = (v.z ^ flip) & keep;
-                            v.w = (v.w ^ flip) & keep;
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)t * a.q_stride +
+                                                                         h * D + c16 * 8));
                         }
+                    }
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        const int r = rr + i * RPP;
+                        uint4 x = make_uint4((v[i].x ^ flip) & keep, (v[i].y ^ flip) & keep,
+                                             (v[i].z ^ flip) & keep, (v[i].w ^ flip) & keep);
                         if constexpr (E4) {
                             // f16, the row's largest entry in [1, 2)
-                            int e = max_exponent(v);
+                            int e = max_exponent(x);
 #pragma unroll
-                            for (int o = 1; o < D / 8; o <<= 1)
+                            for (int o = 1; o < CPR; o <<= 1)
                                 e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
                             const float dn = pow2i(-row_exponent(e));
-                            v = make_uint4(f16_of_bf16(v.x, dn), f16_of_bf16(v.y, dn),
-                                           f16_of_bf16(v.z, dn), f16_of_bf16(v.w, dn));
+                            x = make_uint4(f16_of_bf16(x.x, dn), f16_of_bf16(x.y, dn), f16_of_bf16(x.z, dn),
+                                           f16_of_bf16(x.w, dn));
+                            if (c16 == 0) qpow[(PAIR ? gr * TR : 0) + r] = pow2i(row_exponent(e));
                         }
                         *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * LY::ATOM + r * 128 +
-                                                   (((c16 & 7) ^ (r & 7)) << 4)) = v;
+                                                   (((c16 & 7) ^ (r & 7)) << 4)) = x;
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
                     if constexpr (E4) {                  // the power of two of this thread's row
-                        const int qrow = base + row;
-                        int e = 0;
-                        if (qrow < rows_all && keep) {
-                            const int t = qrow / a.gqa, h = qrow - t * a.gqa;
-                            const uint4 *p = reinterpret_cast<const uint4 *>(
-                                src + (int64_t)t * a.q_stride + h * D);
-#pragma unroll
-                            for (int i = 0; i < D / 8; ++i) e = max(e, max_exponent(__ldg(p + i)));
+                        if (!tc::mbar_wait(&bar->q_full[PAIR ? gr : 0], qn & 1, kWaitNs)) {
+                            ok = false;
+                            break;
                         }
-                        c *= pow2i(row_exponent(e));
+                        c *= qpow[(PAIR ? gr * TR : 0) + row];
                     }
+                    ++qn;
                 }
                 vis -= seg->u0 * TK;                     // from the segment's first key
             }
@@ -902,16 +906,16 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 tc::tc_fence_before();
             }
-            if (!whole) {
-                // every thread's part is visible before this CTA counts itself
-                __threadfence();
-                shared[n_shared++ & 1] = *seg;
-            }
+            if (!whole) shared[n_shared++ & 1] = *seg;
             // SPLIT: Q and group 1's sums may be overwritten once both are here
             if (!PAIR || !whole) {
                 if (!meet(1, met1 & 1)) break;
                 ++met1;
-                if (!whole && tid == 128) tc::red_release_gpu_add(a.count + seg->c0, 1);
+                // every thread's part is written and met here: one releases them all
+                if (!whole && tid == 128) {
+                    __threadfence();
+                    tc::red_release_gpu_add(a.count + seg->c0, 1);
+                }
             }
             ++met;
             close(sg);
@@ -927,12 +931,12 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 bool all = tc::ld_acquire_gpu(count) >= sh.n_ctas;
                 const uint32_t t0 = tc::global_ns_lo();
                 while (!all && tc::global_ns_lo() - t0 < kWaitNs) all = tc::ld_acquire_gpu(count) >= sh.n_ctas;
+                __threadfence();                         // the parts, for the CTA that meets next
                 bar->go = all;
                 if (!all) atomicOr(err, 4);
             }
             if (!meet(1, met1++ & 1)) break;
             const bool all = bar->go != 0;
-            __threadfence();
             if (all) join_rows<D, RB>(a, sh, blockIdx.x - sh.c0, tid - 128);
             if (!meet(1, met1++ & 1)) break;             // go and the counters are free
             if (tid == 128) {
