@@ -32,7 +32,7 @@ struct Lay {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = RB * D;
     static constexpr int FLOATS = OFF_P + NBUF * PAGE;
-    static constexpr int SMEM = FLOATS * 4 + (kMaxSeqs + 3) * 8;
+    static constexpr int SMEM = FLOATS * 4 + (kMaxSeqs + 1) * 4;
 };
 
 }  // namespace
@@ -45,14 +45,18 @@ attend_simt_kernel(AttendArgs a, int min_units) {
     using W = Walk<RB, kBlockTokens>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     float *sm = reinterpret_cast<float *>(smem_raw);
-    int64_t *pre = reinterpret_cast<int64_t *>(sm + LY::FLOATS);
+    int *pre = reinterpret_cast<int *>(sm + LY::FLOATS);
     __shared__ int is_last;
+    __shared__ LineInfo line;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+    if (warp == 0) {
+        const LineInfo li = W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+        if (lane == 0) line = li;
+    }
     __syncthreads();
     W k;
-    if (!k.start(a, pre, cta, gridDim.x, min_units)) return;
+    if (!k.start(a, pre, line, cta, gridDim.x, min_units)) return;
     const int row0 = KS ? 0 : warp * kRows;     // the warp's rows of the tile
     float *kb = sm + LY::OFF_P + (KS ? warp * LY::PAGE : 0), *vb = kb + kBlockTokens * LY::KST;
     do {
@@ -63,7 +67,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
             const int r = i / D, row = rbase + r;
             float v = 0.f;
             if (r < rows) {
-                const int t = row / a.gqa, h = row - t * a.gqa;
+                const int t = token_of(row, a.gqa_inv), h = row - t * a.gqa;
                 v = to_float(typed<TQ>(a.q)[(int64_t)(k.i.q0 + t) * a.q_stride +
                                             (int64_t)(k.g * a.gqa + h) * D + i % D]);
             }
@@ -76,7 +80,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
         for (int r = 0; r < kRows; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-            const int row = rbase + row0 + r, t = row / a.gqa;
+            const int row = rbase + row0 + r, t = token_of(row, a.gqa_inv);
             vis[r] = row0 + r < rows ? (a.causal ? k.i.kv - k.i.q_len + t + 1 : k.i.kv) : 0;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) o[r][c] = 0.f;
@@ -269,7 +273,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
                 if (row0 + r >= rows) continue;
-                const int row = rbase + row0 + r, t = row / a.gqa, h = k.g * a.gqa + row - t * a.gqa;
+                const int row = rbase + row0 + r, t = token_of(row, a.gqa_inv), h = k.g * a.gqa + row - t * a.gqa;
                 const float inv = l[r] > 0.f ? 1.f / l[r] : (l[r] == 0.f ? 0.f : l[r]);
                 TQ *dst = static_cast<TQ *>(a.out) + (int64_t)(k.i.q0 + t) * a.out_stride +
                           (int64_t)h * D + lane * CPL;
@@ -312,9 +316,17 @@ static cudaError_t simt_q(int kv_dtype, const AttendArgs &a, cudaStream_t s) {
 
 size_t attend_scratch_bytes() { return kAttendPartFloats * sizeof(float); }
 
-cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s) {
-    if (attend_decode_supported(q_dtype, kv_dtype, a)) return launch_attend_decode(kv_dtype, a, s);
-    if (attend_tc_supported(q_dtype, kv_dtype, a)) return launch_attend_tc(kv_dtype, a, s);
+cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s,
+                          bool *too_large) {
+    if (attend_decode_supported(q_dtype, kv_dtype, a)) {
+        if (!line_fits(a, 8, kBlockTokens)) return *too_large = true, cudaSuccess;
+        return launch_attend_decode(kv_dtype, a, s);
+    }
+    if (attend_tc_supported(q_dtype, kv_dtype, a)) {
+        if (!line_fits(a, 128, 128)) return *too_large = true, cudaSuccess;
+        return launch_attend_tc(kv_dtype, a, s);
+    }
+    if (!line_fits(a, 4, kBlockTokens)) return *too_large = true, cudaSuccess;
     return q_dtype == BF16 ? simt_q<__nv_bfloat16>(kv_dtype, a, s) : simt_q<float>(kv_dtype, a, s);
 }
 

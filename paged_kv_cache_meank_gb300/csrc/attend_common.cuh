@@ -16,6 +16,10 @@
 
 namespace kvm {
 
+//
+// All of this is run once by one warp before the first load can be issued, from
+// an instruction cache that is cold: it is kept small and in 32 bits (the host
+// checks that the line is shorter than 2^31 units).
 struct SeqInfo {
     int q0, q_len, kv;
 };
@@ -33,149 +37,125 @@ __host__ __device__ __forceinline__ SeqInfo seq_info(const BatchArgs &b, int s, 
     return i;
 }
 
+// The token of a query row (row / gqa): `inv` is ceil(2^32 / gqa), or 0 for 1;
+// exact while row * gqa < 2^32, which the host checks.
+__host__ __device__ __forceinline__ int token_of(int row, uint32_t inv) {
+    return inv ? (int)(((uint64_t)(uint32_t)row * inv) >> 32) : row;
+}
+
+// A line of units, as laid out (see lay_out).
+struct LineInfo {
+    int total;     // units of all
+    int most;      // the largest row tile's
+    int pad;       // units every row tile is counted as, or 0: its own
+};
+
 template <int RB, int UNIT>
 struct Line {
     // Keys that row tile r of a sequence sees (its last row sees the most).
-    __host__ __device__ static __forceinline__ int keys(const SeqInfo &i, int gqa, int causal, int r) {
-        if (!causal) return i.kv;
-        const int row_end = min(i.q_len * gqa, (r + 1) * RB);
-        return max(0, min(i.kv, i.kv - i.q_len + (row_end - 1) / gqa + 1));
+    __host__ __device__ static __forceinline__ int keys(const SeqInfo &i, const AttendArgs &a, int r) {
+        if (!a.causal) return i.kv;
+        const int row_end = min(i.q_len * a.gqa, (r + 1) * RB);
+        return max(0, min(i.kv, i.kv - i.q_len + token_of(row_end - 1, a.gqa_inv) + 1));
     }
-    __host__ __device__ static __forceinline__ int tiles(const SeqInfo &i, int gqa) {
-        return (i.q_len * gqa + RB - 1) / RB;
+    __host__ __device__ static __forceinline__ int tiles(const SeqInfo &i, const AttendArgs &a) {
+        return (i.q_len * a.gqa + RB - 1) / RB;
     }
-    __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, int gqa, int causal, int r) {
-        return max(1, (keys(i, gqa, causal, r) + UNIT - 1) / UNIT);
+    __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, const AttendArgs &a, int r) {
+        return max(1, (keys(i, a, r) + UNIT - 1) / UNIT);
     }
-    // A sequence's units by one head, as summed by the lane (few row tiles) or the
-    // warp; every lane of the warp calls it with its sequence's lengths.
-    __device__ static int64_t units(const SeqInfo &i, int gqa, int causal, int n_here, int lane) {
-        const int n = tiles(i, gqa);
-        int64_t w = 0;
-        if (__all_sync(0xffffffffu, n <= 8)) {
-            for (int r = 0; r < n; ++r) w += weight(i, gqa, causal, r);
-            return w;
-        }
-        for (int x = 0; x < n_here; ++x) {
-            SeqInfo j;
-            j.q0 = 0;
-            j.q_len = __shfl_sync(0xffffffffu, i.q_len, x);
-            j.kv = __shfl_sync(0xffffffffu, i.kv, x);
-            const int m = tiles(j, gqa);
-            int64_t sum = 0;
-            for (int r = lane; r < m; r += 32) sum += weight(j, gqa, causal, r);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == x) w = sum;
-        }
-        return w;
-    }
-    // Lays the line out: pre[s] = units of the sequences before s, pre[n_seqs] =
-    // all, pre[n_seqs + 1] = the largest tile's, pre[n_seqs + 2] = the units every
-    // tile is counted as, or 0 for its own (see run_units).  By one warp.
+    // Lays the line out: pre[s] = units of the sequences before s (pre: kMaxSeqs
+    // + 1 in shared memory).  By one warp, a lane to a sequence.
     template <bool PAD>
-    __device__ static void lay_out(const AttendArgs &a, int64_t *pre, int n_ctas, int min_units) {
+    __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units) {
         const int lane = threadIdx.x & 31;
-        int64_t run = 0, items = 0;
-        int most = 1;
-        for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
-            const int s = s0 + lane;
-            SeqInfo i{0, 0, 0};
-            bool ok = true;
-            if (s < a.b.n_seqs) i = seq_info(a.b, s, &ok);
-            if (!ok) atomicOr(a.b.err, kErrBatch);
-            const int n = tiles(i, a.gqa);
-            if (n > 0) most = max(most, weight(i, a.gqa, a.causal, n - 1));   // the last sees most
-            int64_t w = units(i, a.gqa, a.causal, min(32, a.b.n_seqs - s0), lane) * a.b.G;
-            int64_t m = (int64_t)n * a.b.G;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
-                const int64_t um = __shfl_up_sync(0xffffffffu, m, o);
-                if (lane >= o) {
-                    w += up;
-                    m += um;
-                }
-            }
-            if (s < a.b.n_seqs) pre[s + 1] = run + w;
-            run += __shfl_sync(0xffffffffu, w, 31);
-            items += __shfl_sync(0xffffffffu, m, 31);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-        int pad = 0;
-        if (PAD) pad = padded_weight(items, run, most, n_ctas, min_units);
-        if (pad) {
-            // every tile counts alike: the prefix sums again, by tiles
-            run = 0;
+        LineInfo li{0, 1, 0};
+        for (int pass = 0; pass < 2; ++pass) {
+            int run = 0, items = 0;
+#pragma unroll 1
             for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
                 const int s = s0 + lane;
-                bool ok;
-                int64_t w = s < a.b.n_seqs ? (int64_t)tiles(seq_info(a.b, s, &ok), a.gqa) * a.b.G * pad : 0;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
-                    if (lane >= o) w += up;
+                int w = 0, n = 0;
+                if (s < a.b.n_seqs) {
+                    bool ok;
+                    const SeqInfo i = seq_info(a.b, s, &ok);
+                    if (!ok) atomicOr(a.b.err, kErrBatch);
+                    n = tiles(i, a);
+                    if (pass) {
+                        w = n * li.pad;
+                    } else {
+#pragma unroll 1
+                        for (int r = 0; r < n; ++r) {
+                            const int x = weight(i, a, r);
+                            w += x;
+                            li.most = max(li.most, x);
+                        }
+                    }
+                }
+                w *= a.b.G;
+                n *= a.b.G;
+                if (a.b.n_seqs > 1) {
+#pragma unroll 1
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int up = __shfl_up_sync(0xffffffffu, w, o);
+                        const int un = __shfl_up_sync(0xffffffffu, n, o);
+                        if (lane >= o) {
+                            w += up;
+                            n += un;
+                        }
+                    }
                 }
                 if (s < a.b.n_seqs) pre[s + 1] = run + w;
-                run += __shfl_sync(0xffffffffu, w, 31);
+                const int last = a.b.n_seqs > 1 ? 31 : 0;
+                run += __shfl_sync(0xffffffffu, w, last);
+                items += __shfl_sync(0xffffffffu, n, last);
+            }
+            li.total = run;
+            if (pass == 0) {
+                li.most = __reduce_max_sync(0xffffffffu, li.most);
+                if (!PAD || (li.pad = padded_weight(items, li, n_ctas, min_units)) == 0) break;
             }
         }
-        if (lane == 0) {
-            pre[0] = 0;
-            pre[a.b.n_seqs + 1] = most;
-            pre[a.b.n_seqs + 2] = pad;
-        }
+        if (lane == 0) pre[0] = 0;
         __syncwarp();
+        return li;
     }
     // Where the row tiles are about equally long, they are all counted as `pad`
     // units, at least the longest one's: runs then begin and end at the same few
     // places of every tile (run_units).  A CTA meets one tile and not the ends of
     // two, and CTAs that share a head's keys read them at the same time (begun at
     // scattered keys they read 762 MB of a 134 MB cache).
-    __host__ __device__ static int padded_weight(int64_t items, int64_t total, int most, int n_ctas,
-                                                 int min_units) {
-        if (items == 0 || total * 100 < items * most * 85) return 0;
-        if (items * 4 < (int64_t)n_ctas * 3) {           // several CTAs to a tile
-            const int least = most < min_units ? most : min_units;
-            int parts = (int)(n_ctas / items);
-            if (parts > most / least) parts = most / least;
-            return (most + parts - 1) / parts * parts;
+    __host__ __device__ static int padded_weight(int items, const LineInfo &li, int n_ctas, int min_units) {
+        if (items == 0 || (float)li.total < 0.85f * (float)items * (float)li.most) return 0;
+        if (items * 4 < n_ctas * 3) {                    // several CTAs to a tile
+            const int parts = min(n_ctas / items, li.most / min(li.most, min_units));
+            return (li.most + parts - 1) / parts * parts;
         }
-        const int pad = (most + 11) / 12 * 12;
-        return most >= 24 && total * 100 >= items * pad * 85 ? pad : 0;
+        const int pad = (li.most + 11) / 12 * 12;
+        return li.most >= 24 && (float)li.total >= 0.85f * (float)items * (float)pad &&
+                       (float)items * (float)pad < 2147483647.f
+                   ? pad
+                   : 0;
     }
 };
-
-// a / b, both >= 0: 32-bit division where they fit (a 64-bit one takes about 10
-// times as long, and a walk has several before its first load).
-__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
-    return a / b;
-}
 
 // Units of one CTA's run: an equal share, but not so small that a tile's join
 // costs more than its keys, unless whole tiles are smaller.  Of tiles counted
 // alike, a CTA takes an equal part of one, or with more tiles than CTAs a
 // multiple of a whole, a half, a third or a quarter: the first of these that
 // gives away at most 1/16 of the share, else the one that gives away least.
-__host__ __device__ __forceinline__ int64_t run_units(const AttendArgs &a, const int64_t *pre, int n_ctas,
-                                                      int min_units) {
-    const int64_t share = quotient(pre[a.b.n_seqs] + n_ctas - 1, n_ctas);
-    const int64_t most = pre[a.b.n_seqs + 1], least = most < min_units ? most : min_units;
-    const int64_t pad = pre[a.b.n_seqs + 2];
-    if (!pad) return share > least ? share : least;
-    const int64_t items = quotient(pre[a.b.n_seqs], pad);
-    if (items * 4 < (int64_t)n_ctas * 3) {
-        int64_t parts = quotient(n_ctas, items);
-        if (parts > quotient(most, least)) parts = quotient(most, least);
-        return quotient(pad, parts);
-    }
-    int64_t best = 0;
+__host__ __device__ __forceinline__ int run_units(const LineInfo &li, int n_ctas, int min_units) {
+    const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
+    const int least = min(li.most, min_units);
+    if (!li.pad) return max(share, least);
+    const int items = li.total / li.pad;
+    if (items * 4 < n_ctas * 3) return li.pad / min(n_ctas / items, li.most / least);
+    int best = 0;
+#pragma unroll 1
     for (int m = 1; m <= 4; ++m) {
-        const int64_t part = pad / m, run = quotient(share + part - 1, part) * part;
+        const int part = li.pad / m, run = (share + part - 1) / part * part;
         if (best == 0 || run < best) best = run;
-        if (run * 16 <= share * 17) return run;
+        if (run - share <= share / 16) return run;
     }
     return best;
 }
@@ -184,60 +164,51 @@ __host__ __device__ __forceinline__ int64_t run_units(const AttendArgs &a, const
 template <int RB, int UNIT>
 struct Walk {
     using LN = Line<RB, UNIT>;
-    int64_t x, end, per;     // position, end of the run, units of a run
+    int x, end, per;         // position, end of the run, units of a run
     int s, g, r, n_tiles;    // sequence, kv head, row tile
     int u0, u1, w, pad;      // the segment's units [u0, u1) of the tile's w (pad: as counted)
     int nk;                  // keys the tile sees
     SeqInfo i;
 
-    // per: units of one CTA's run.  False when the run is empty.
-    __host__ __device__ __forceinline__ bool start(const AttendArgs &a, const int64_t *pre, int cta,
-                                          int n_ctas, int min_units) {
-        const int64_t total = pre[a.b.n_seqs];
-        per = run_units(a, pre, n_ctas, min_units);
-        if (cta * per >= total) return false;
-        start_at(a, pre, cta * per, per);
-        end = min(total, x + per);
-        fill(a);
-        return true;
-    }
-    // The position of one unit of the line; the run ends with that unit.
-    __host__ __device__ __forceinline__ void start_at(const AttendArgs &a, const int64_t *pre,
-                                                      int64_t at, int64_t per_) {
-        x = at;
-        per = per_;
-        end = at + 1;
+    // False when the CTA's run is empty.
+    __host__ __device__ __forceinline__ bool start(const AttendArgs &a, const int *pre, const LineInfo &li,
+                                                   int cta, int n_ctas, int min_units) {
+        per = run_units(li, n_ctas, min_units);
+        if ((int64_t)cta * per >= li.total) return false;
+        x = cta * per;
+        end = li.total - x < per ? li.total : x + per;
         int lo = 0, hi = a.b.n_seqs - 1;                // the last s with pre[s] <= x
         while (lo < hi) {
             const int m = (lo + hi + 1) >> 1;
             if (pre[m] <= x) lo = m; else hi = m - 1;
         }
         s = lo;
-        pad = (int)pre[a.b.n_seqs + 2];
+        pad = li.pad;
         bool ok;
         i = seq_info(a.b, s, &ok);
-        n_tiles = LN::tiles(i, a.gqa);
-        int64_t rem = x - pre[s];
-        const int64_t per_head = quotient(pre[s + 1] - pre[s], a.b.G);
-        g = (int)quotient(rem, per_head);
+        n_tiles = LN::tiles(i, a);
+        int rem = x - pre[s];
+        const int per_head = (pre[s + 1] - pre[s]) / a.b.G;
+        g = rem / per_head;
         rem -= g * per_head;
-        r = 0;
         if (pad) {
-            r = (int)quotient(rem, pad);
-            rem -= (int64_t)r * pad;
-            w = pad;
+            r = rem / pad;
+            rem -= r * pad;
         } else {
-            for (w = LN::weight(i, a.gqa, a.causal, 0); rem >= w; w = LN::weight(i, a.gqa, a.causal, r)) {
-                rem -= w;
+            r = 0;
+            for (int y = LN::weight(i, a, 0); rem >= y; y = LN::weight(i, a, r)) {
+                rem -= y;
                 ++r;
             }
         }
-        u0 = (int)rem;
+        u0 = rem;
         fill(a);
+        return true;
     }
     __host__ __device__ __forceinline__ void fill(const AttendArgs &a) {
-        nk = LN::keys(i, a.gqa, a.causal, r);
-        u1 = (int)min((int64_t)w, u0 + (end - x));
+        w = pad ? pad : LN::weight(i, a, r);
+        nk = LN::keys(i, a, r);
+        u1 = min(w, u0 + (end - x));
     }
     __host__ __device__ __forceinline__ bool next(const AttendArgs &a) {
         x += u1 - u0;
@@ -250,24 +221,31 @@ struct Walk {
                 do {                                    // skips sequences without rows
                     bool ok;
                     i = seq_info(a.b, ++s, &ok);
-                    n_tiles = LN::tiles(i, a.gqa);
+                    n_tiles = LN::tiles(i, a);
                 } while (n_tiles == 0);
             }
         }
-        w = pad ? pad : LN::weight(i, a.gqa, a.causal, r);
         fill(a);
         return true;
     }
     // Key tiles of the segment: its units that hold keys.
     __host__ __device__ __forceinline__ int key_units() const {
         const int real = (nk + UNIT - 1) / UNIT;
-        return (u1 < real ? u1 : real) - (u0 < real ? u0 : real);
+        return min(u1, real) - min(u0, real);
     }
     __host__ __device__ __forceinline__ bool whole() const { return u0 == 0 && u1 == w; }
     // The first and last CTA that share the segment's tile.
-    __host__ __device__ __forceinline__ int first_cta() const { return (int)quotient(x - u0, per); }
-    __host__ __device__ __forceinline__ int last_cta() const { return (int)quotient(x - u0 + w - 1, per); }
+    __host__ __device__ __forceinline__ int first_cta() const { return (x - u0) / per; }
+    __host__ __device__ __forceinline__ int last_cta() const { return (x - u0 + w - 1) / per; }
 };
+
+// Whether a call's bounds keep the line and the query rows in their 32 bits.
+inline bool line_fits(const AttendArgs &a, int rb, int unit) {
+    const double rows = (double)a.b.max_q_len * a.gqa;
+    const double tiles = (double)a.b.n_seqs * a.b.G * ((int64_t)(rows + rb - 1) / rb);
+    return tiles * ((a.b.max_kv_len + (double)unit) / unit + 12) < 2147483647.0 &&
+           rows * a.gqa < 4294967296.0;
+}
 
 // A CTA's two places for partial results: 1 for a tile that goes on in the next
 // CTA and begins in this one, 0 for a tile that began in an earlier one.

@@ -46,7 +46,7 @@ struct Lay {
     static constexpr int ORS = D + 4;                      // a row of a warp's joined output
     static constexpr int REC = RB * ORS + 2 * RB;          // floats: o, m, l
     static constexpr int BYTES = WARPS * (RING > REC * 4 ? RING : REC * 4);
-    static constexpr int SMEM = BYTES + (kMaxSeqs + 3) * 8;
+    static constexpr int SMEM = BYTES + (kMaxSeqs + 1) * 4;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -117,15 +117,19 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     constexpr int CH = LY::ROW / 16;                       // 16-byte chunks of a row
     using W = Walk<RB, kBlockTokens>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    int64_t *pre = reinterpret_cast<int64_t *>(smem + LY::BYTES);
+    int *pre = reinterpret_cast<int *>(smem + LY::BYTES);
     __shared__ int is_last;
+    __shared__ LineInfo line;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
     const int cta = blockIdx.x;
-    if (warp == 0) W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+    if (warp == 0) {
+        const LineInfo li = W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+        if (lane == 0) line = li;
+    }
     __syncthreads();
     W k;
-    if (!k.start(a, pre, cta, gridDim.x, min_units)) return;
+    if (!k.start(a, pre, line, cta, gridDim.x, min_units)) return;
     uint8_t *ring = smem + warp * LY::RING;
     const uint32_t ring32 = tc::smem_u32(ring);
     const float c = a.scale * kLog2e;
@@ -147,7 +151,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
             const int r = t * 8 + g8, row = rbase + r;
             const __nv_bfloat16 *src = nullptr;
             if (r < rows) {
-                const int tok = row / a.gqa, h = row - tok * a.gqa;
+                const int tok = token_of(row, a.gqa_inv), h = row - tok * a.gqa;
                 src = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(k.i.q0 + tok) * a.q_stride +
                       (int64_t)(k.g * a.gqa + h) * D;
             }
@@ -191,12 +195,12 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int q = t * 8 + c4 * 2 + b, tok = (rbase + q) / a.gqa;
+                const int q = t * 8 + c4 * 2 + b, tok = token_of(rbase + q, a.gqa_inv);
                 vis[t][b] = q >= rows ? 0 : a.causal ? min(k.i.kv, k.i.kv - k.i.q_len + tok + 1) : k.i.kv;
             }
         }
         // keys below `all` are seen by every row of the tile
-        const int all = a.causal ? k.i.kv - k.i.q_len + rbase / a.gqa + 1 : k.i.kv;
+        const int all = a.causal ? k.i.kv - k.i.q_len + token_of(rbase, a.gqa_inv) + 1 : k.i.kv;
         float m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -471,7 +475,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
         float *part = a.part + part_slot(cta, cta == c0) * PREC;
         const float *all_rec = reinterpret_cast<const float *>(smem);
         auto put = [&](int r, int q, float4 v, float mm, float ll) {   // the finished row's quad q
-            const int row = rbase + r, tok = row / a.gqa, h = k.g * a.gqa + row - tok * a.gqa;
+            const int row = rbase + r, tok = token_of(row, a.gqa_inv), h = k.g * a.gqa + row - tok * a.gqa;
             const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
                                  (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D + q * 4;

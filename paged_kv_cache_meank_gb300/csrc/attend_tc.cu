@@ -74,7 +74,7 @@ struct Lay {
     static constexpr int OFF_BAR = OFF_QP + (E4 ? Q_TILES * TR * 4 : 0);
     static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
-    static_assert(SLOTS * TILE >= (kMaxSeqs + 3) * 8, "prefix fits the ring");
+    static_assert(SLOTS * TILE >= (kMaxSeqs + 1) * 4, "prefix fits the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -196,6 +196,7 @@ __device__ __forceinline__ void join_quads(const AttendArgs &a, const Seg &sh, i
         l[u] = 0.f;
         o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll 1
     for (int p0 = 0; p0 < n; p0 += P) {
         float pm[P][U], pl[P][U];
         float4 v[P][U];
@@ -229,7 +230,7 @@ __device__ __forceinline__ void join_quads(const AttendArgs &a, const Seg &sh, i
     for (int u = 0; u < U; ++u) {
         if (x + u * 256 > last) continue;
         const float inv = l[u] > 0.f ? 1.f / l[u] : (l[u] == 0.f ? 0.f : l[u]);
-        const int qrow = sh.rbase + row[u], tok = qrow / a.gqa, h = sh.g * a.gqa + qrow - tok * a.gqa;
+        const int qrow = sh.rbase + row[u], tok = token_of(qrow, a.gqa_inv), h = sh.g * a.gqa + qrow - tok * a.gqa;
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
                                    (int64_t)(sh.q0 + tok) * a.out_stride + (int64_t)h * D + q[u] * 4) =
             make_uint2(pack_bf16(o[u].x * inv, o[u].y * inv), pack_bf16(o[u].z * inv, o[u].w * inv));
@@ -244,10 +245,8 @@ template <int D, int RB>
 __device__ __forceinline__ void join_rows(const AttendArgs &a, const Seg &sh, int part, int t) {
     const int rows = min(RB, sh.q_len * a.gqa - sh.rbase), n = sh.n_ctas;
     const int r0 = rows * part / n, nr = rows * (part + 1) / n - r0;
-    if (n <= 4)
-        for (int x = t; x < nr * (D / 4); x += 256 * 4) join_quads<D, RB, 4, 4>(a, sh, r0, nr, x);
-    else
-        for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 10>(a, sh, r0, nr, x);
+#pragma unroll 1
+    for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 4>(a, sh, r0, nr, x);
 }
 
 }  // namespace
@@ -531,10 +530,10 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             // ---------------------------------------------------- the walk
             using W = Walk<RB, TK>;
             // the prefix sums live in the ring: its first copies follow the first segment
-            int64_t *pre = reinterpret_cast<int64_t *>(kvs);
-            W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
+            int *pre = reinterpret_cast<int *>(kvs);
+            const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
             W k;
-            bool any = k.start(a, pre, blockIdx.x, gridDim.x, min_units);
+            bool any = k.start(a, pre, li, blockIdx.x, gridDim.x, min_units);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
@@ -598,7 +597,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             {
                 const int q_len = seg->q_len, kv = seg->kv, rows_all = q_len * a.gqa;
                 const int base = seg->rbase + (PAIR ? gr * TR : 0);
-                vis = a.causal ? min(kv, kv - q_len + (base + row) / a.gqa + 1) : kv;
+                vis = a.causal ? min(kv, kv - q_len + token_of(base + row, a.gqa_inv) + 1) : kv;
                 if (T > 0) {
                     // this group's query rows (SPLIT: its half) into the swizzled layout;
                     // nobody reads the last segment's any more
@@ -607,38 +606,44 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                                (int64_t)seg->q0 * a.q_stride +
                                                (int64_t)seg->g * a.gqa * D;
+                    // four loads in flight at a time, in a loop: unrolled whole, fetching its
+                    // instructions took three times as long as the loads
                     constexpr int CPR = D / 8, RPP = 128 / CPR;       // chunks of a row, rows of a pass
                     constexpr int N = (PAIR ? TR : TR / 2) / RPP;     // a thread's chunks
                     const int c16 = (tid & 127) % CPR, rr = r0 + (tid & 127) / CPR;
-                    uint4 v[N];                          // all loads in flight together
+                    src += c16 * 8;
+                    dst += (c16 >> 3) * LY::ATOM;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < N; i0 += 4) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int qrow = base + rr + i * RPP;
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (qrow < rows_all) {
-                            const int t = qrow / a.gqa, h = qrow - t * a.gqa;
-                            v[i] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)t * a.q_stride +
-                                                                         h * D + c16 * 8));
+                        for (int i = 0; i < 4; ++i) {
+                            const int qrow = base + rr + (i0 + i) * RPP;
+                            v[i] = make_uint4(0, 0, 0, 0);
+                            if (qrow < rows_all) {
+                                const int t = token_of(qrow, a.gqa_inv), h = qrow - t * a.gqa;
+                                v[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                    src + (int64_t)t * a.q_stride + h * D));
+                            }
                         }
-                    }
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int r = rr + i * RPP;
-                        uint4 x = make_uint4((v[i].x ^ flip) & keep, (v[i].y ^ flip) & keep,
-                                             (v[i].z ^ flip) & keep, (v[i].w ^ flip) & keep);
-                        if constexpr (E4) {
-                            // f16, the row's largest entry in [1, 2)
-                            int e = max_exponent(x);
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = rr + (i0 + i) * RPP;
+                            uint4 x = make_uint4((v[i].x ^ flip) & keep, (v[i].y ^ flip) & keep,
+                                                 (v[i].z ^ flip) & keep, (v[i].w ^ flip) & keep);
+                            if constexpr (E4) {
+                                // f16, the row's largest entry in [1, 2)
+                                int e = max_exponent(x);
 #pragma unroll
-                            for (int o = 1; o < CPR; o <<= 1)
-                                e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-                            const float dn = pow2i(-row_exponent(e));
-                            x = make_uint4(f16_of_bf16(x.x, dn), f16_of_bf16(x.y, dn), f16_of_bf16(x.z, dn),
-                                           f16_of_bf16(x.w, dn));
-                            if (c16 == 0) qpow[(PAIR ? gr * TR : 0) + r] = pow2i(row_exponent(e));
+                                for (int o = 1; o < CPR; o <<= 1)
+                                    e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+                                const float dn = pow2i(-row_exponent(e));
+                                x = make_uint4(f16_of_bf16(x.x, dn), f16_of_bf16(x.y, dn),
+                                               f16_of_bf16(x.z, dn), f16_of_bf16(x.w, dn));
+                                if (c16 == 0) qpow[(PAIR ? gr * TR : 0) + r] = pow2i(row_exponent(e));
+                            }
+                            *reinterpret_cast<uint4 *>(dst + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = x;
                         }
-                        *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * LY::ATOM + r * 128 +
-                                                   (((c16 & 7) ^ (r & 7)) << 4)) = x;
                     }
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
@@ -847,7 +852,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 tc::tc_fence_after();
                 const int prow = (PAIR ? gr * TR : 0) + row, qrow = seg->rbase + prow;
                 const bool live = qrow < seg->q_len * a.gqa;
-                const int tok = qrow / a.gqa, h = seg->g * a.gqa + qrow - tok * a.gqa;
+                const int tok = token_of(qrow, a.gqa_inv), h = seg->g * a.gqa + qrow - tok * a.gqa;
                 float *rec = a.part + part_slot(blockIdx.x, seg->first) * ((size_t)RB * (D + 2));
                 if (whole) {
                     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);

@@ -256,6 +256,7 @@ cudaError_t launch_append(int q_dtype, int kv_dtype, int d, const AppendArgs &a,
 struct AttendArgs {
     BatchArgs b;
     int H, gqa, d;
+    uint32_t gqa_inv;              // see token_of
     const void *q;
     int64_t q_stride;
     const void *k_pages, *v_pages;
@@ -270,7 +271,9 @@ struct AttendArgs {
 };
 constexpr int kAttendMaxCtas = 608;    // CTAs of one attention grid, at most
 size_t attend_scratch_bytes();         // of AttendArgs::part
-cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s);
+// Sets *too_large instead of launching where the call's bounds are beyond 32 bits.
+cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s,
+                          bool *too_large);
 
 // Multiprocessors of the current device (152 where it cannot be read).
 int sm_count();

@@ -265,6 +265,7 @@ kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cac
     KVM_TRY(on_device(lse, c, "lse", false));
     a.H = c.H;
     a.gqa = c.H / c.G;
+    a.gqa_inv = a.gqa > 1 ? (uint32_t)(((1ull << 32) + a.gqa - 1) / a.gqa) : 0;
     a.d = c.d;
     a.q = q;
     a.q_stride = q_stride;
@@ -279,9 +280,13 @@ kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cac
     a.lse = lse;
     a.part = c.attend_part;
     a.count = c.attend_count;
-    return launched(
-        kvm::launch_attend(c.q_dtype, c.kv_dtype, a, reinterpret_cast<cudaStream_t>(stream)),
-        "attention launch");
+    bool too_large = false;
+    const cudaError_t e = kvm::launch_attend(c.q_dtype, c.kv_dtype, a,
+                                             reinterpret_cast<cudaStream_t>(stream), &too_large);
+    if (too_large)
+        return fail(KVM_ERR_CAPACITY, "batch: %d sequences of up to %d x %d tokens are too much for one call",
+                    batch->n_seqs, batch->max_q_len, batch->max_kv_len);
+    return launched(e, "attention launch");
 }
 
 kvm_status kvm_build_index_scaled(kvm_ctx *ctx, const void *k_pages, const float *k_scale,
