@@ -3,11 +3,11 @@
 // head.  The cache is read once and each byte of it meets 16 rows at most, so
 // the kernel is bound by HBM; what counts is loads in flight.
 //
-// A warp owns every n-th stage of its CTA's run of keys (16 or 32 keys of K and
-// V, 4-8 KB) with a ring of cp.async stages of its own in shared memory, its own
-// running maximum, weight and output, and no barrier until the run's end.  Keys
-// take the 16-row side of mma.m16n8k16 and query rows the 8-column side, so one
-// kv head's 6 or 8 rows fill it:
+// A warp owns every fourth stage of its CTA's run of keys (16 or 32 keys of K
+// and V, 4-8 KB) with a ring of cp.async stages of its own in shared memory, its
+// own running maximum, weight and output, and no barrier until the run's end.
+// Keys take the 16-row side of mma.m16n8k16 and query rows the 8-column side, so
+// one kv head's 6 or 8 rows fill it:
 //   S^T[16 keys][8 rows]  = K Q^T      K by ldmatrix, Q in registers
 //   O^T[16 d][8 rows]    += V^T P^T    V by transposing ldmatrix, P^T from S^T by
 //                                      movmatrix
@@ -16,10 +16,13 @@
 // attend_tc.cu the maximum moves when a stage exceeds it by 2^8; a vote decides,
 // so the usual stage has no shuffles.
 //
-// e4m3: codes become f16 (exact) in registers, so products run in f16 with P
-// rounded to 11 bits; q is scaled per row to [1, 2) first (a power of two), and
-// the page's k_scale goes into the exponent's factor.  v_scale multiplies the
-// page's own product in float32, so scales of any size keep their precision.
+// e4m3: as in attend_tc.cu codes become f16 (exact) in registers, q is divided by
+// a power of two per row, the page's k_scale goes into the factor of the scores
+// and the weights times v_scale have a running maximum of their own.
+//
+// Rows of 256 bytes (bf16, d = 128): two CTAs an SM with three 8 KB stages a
+// warp.  Narrower rows carry more arithmetic for their bytes: three CTAs with
+// four 4 KB stages a warp.
 #include <math.h>
 
 #include "attend_common.cuh"
@@ -34,18 +37,22 @@ constexpr float kMoveMax = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D, bool E4, int NT, int WARPS>
+constexpr int kWarps = 4;
+constexpr int kMinPages = 8;               // of a CTA's run: below, a join costs more than the keys
+
+template <int D, bool E4, int NT>
 struct Lay {
     static constexpr int RB = 8 * NT;
     static constexpr int ROW = E4 ? D : 2 * D;             // bytes of a K or V row
-    static constexpr int KEYS = ROW == 256 ? 16 : 32;      // keys of a stage
+    static constexpr int KEYS = ROW == 64 ? 32 : 16;       // keys of a stage
     static constexpr int HALF = KEYS * ROW;                // K (or V) of a stage
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int STAGES = STAGE == 8192 ? 3 : 6;
+    static constexpr int STAGES = STAGE == 8192 ? 3 : 4;
+    static constexpr int CTAS = NT == 1 && ROW < 256 ? 3 : 2;   // of an SM
     static constexpr int RING = STAGES * STAGE;            // of one warp
-    static constexpr int ORS = D + 4;                      // a row of a warp's joined output
+    static constexpr int ORS = D + 4;                      // a row of a warp's sums
     static constexpr int REC = RB * ORS + 2 * RB;          // floats: o, m, l
-    static constexpr int BYTES = WARPS * (RING > REC * 4 ? RING : REC * 4);
+    static constexpr int BYTES = kWarps * (RING > REC * 4 ? RING : REC * 4);
     static constexpr int SMEM = BYTES + (kMaxSeqs + 1) * 4;
 };
 
@@ -99,21 +106,21 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two e4m3 codes (low 16 bits) as f16x2: exact.
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-    return r;
+// Four e4m3 codes as two f16x2: exact.
+__device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 }  // namespace
 
-template <int D, bool E4, int NT, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32)
+template <int D, bool E4, int NT>
+__global__ void __launch_bounds__(kWarps * 32, Lay<D, E4, NT>::CTAS)
 attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
-    using LY = Lay<D, E4, NT, WARPS>;
+    using LY = Lay<D, E4, NT>;
     constexpr int RB = LY::RB, KS = D / 16, MT = D / 16, KEYS = LY::KEYS, S = LY::STAGES;
-    constexpr int SPP = kBlockTokens / KEYS;               // stages of a page
     constexpr int CH = LY::ROW / 16;                       // 16-byte chunks of a row
     using W = Walk<RB, kBlockTokens>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -124,14 +131,13 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
     const int cta = blockIdx.x;
     if (warp == 0) {
-        const LineInfo li = W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+        const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
         if (lane == 0) line = li;
     }
     __syncthreads();
     W k;
     if (!k.start(a, pre, line, cta, gridDim.x, min_units)) return;
-    uint8_t *ring = smem + warp * LY::RING;
-    const uint32_t ring32 = tc::smem_u32(ring);
+    const uint32_t ring32 = tc::smem_u32(smem + warp * LY::RING);
     const float c = a.scale * kLog2e;
     // a chunk's place in its row: the 8 rows that an ldmatrix phase reads at one
     // chunk fall into distinct banks (rows of 64 bytes: two to a bank line)
@@ -142,6 +148,67 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     do {
         const int rows_all = k.i.q_len * a.gqa, rbase = k.r * RB;
         const int rows = min(RB, rows_all - rbase);
+        // ---- the warp's stages: numbers warp, warp + kWarps, ... of the run
+        const int key_first = k.u0 * kBlockTokens;
+        const int key_end = min(k.nk, k.u1 * kBlockTokens);
+        const int n_all = key_end > key_first ? (key_end - key_first + KEYS - 1) / KEYS : 0;
+        const int n = n_all > warp ? (n_all - warp + kWarps - 1) / kWarps : 0;
+        int32_t page_of = -1;                              // lane i: page of the batch's stage i
+        float ks_of = 1.f, vs_of = 1.f;
+        auto look_up = [&](int j0) {                       // 32 stages' pages and scales
+            const int j = j0 + lane;
+            page_of = -1;
+            if (j < n) {
+                const int p = (key_first + (warp + j * kWarps) * KEYS) / kBlockTokens;
+                const int64_t at = (int64_t)k.s * a.b.table_stride + p;
+                const int32_t page = a.b.page_table[at];
+                bool ok = page >= 0 && page < a.b.n_pages;
+                if (E4 && a.k_scale) {
+                    const int64_t r = a.b.scale_rows ? (int64_t)a.b.scale_rows[at] : (int64_t)page;
+                    ok = ok && r >= 0 && r < a.b.n_scale_rows;
+                    if (ok) {
+                        const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + k.g;
+                        ks_of = checked_scale(a.k_scale[so], a.b.err);
+                        vs_of = checked_scale(a.v_scale[so], a.b.err);
+                    }
+                }
+                if (ok) page_of = page;
+                else atomicOr(a.b.err, kErrBatch);
+            }
+        };
+        float ks_q[S - 1], lv_q[S - 1];                    // k_scale, log2 v_scale of the stages in flight
+        auto issue = [&](int j, int slot) {
+            if (j < n) {
+                const int32_t page = __shfl_sync(0xffffffffu, page_of, j & 31);
+                const int key0 = key_first + (warp + j * kWarps) * KEYS;
+                const int64_t head = ((int64_t)max(page, 0) * a.b.L + a.b.layer) * a.b.G + k.g;
+                const int64_t off = (head * kBlockTokens + (key0 & (kBlockTokens - 1))) * LY::ROW + lane * 16;
+                const char *kp = static_cast<const char *>(a.k_pages) + off;
+                const char *vp = static_cast<const char *>(a.v_pages) + off;
+                const uint32_t dst = ring32 + slot * LY::STAGE;
+                const int n_rows = page >= 0 ? k.i.kv - key0 : 0;   // rows behind them read as 0
+#pragma unroll
+                for (int i = 0; i < LY::HALF / 512; ++i) {
+                    const int x = i * 32 + lane, row = x / CH, at = place(row, x % CH);
+                    copy16(dst + at, kp + i * 512, row < n_rows);
+                    copy16(dst + LY::HALF + at, vp + i * 512, row < n_rows);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if constexpr (E4) {
+#pragma unroll
+                for (int i = 0; i + 1 < S - 1; ++i) {
+                    ks_q[i] = ks_q[i + 1];
+                    lv_q[i] = lv_q[i + 1];
+                }
+                ks_q[S - 2] = __shfl_sync(0xffffffffu, ks_of, j & 31);
+                lv_q[S - 2] = (float)((int)(__float_as_uint(__shfl_sync(0xffffffffu, vs_of, j & 31)) >> 23) - 127);
+            }
+        };
+        look_up(0);
+#pragma unroll 1
+        for (int i = 0; i < S - 1; ++i) issue(i, i);
+
         // ---- the query rows as B fragments, and what each score is multiplied by
         uint32_t qf[NT][KS][2];
         float cm[NT][2];
@@ -167,22 +234,21 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
             } else {
                 // d = 16 s + 4 c4 + {0, 1 | 2, 3}: the order a code quad is held in
                 uint2 w[KS];
-                float mx = 0.f;
+                uint32_t e = 0;
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     w[s] = src ? __ldg(reinterpret_cast<const uint2 *>(src + s * 16 + c4 * 4))
                                : make_uint2(0, 0);
-                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(w[s].x << 16)),
-                                               fabsf(__uint_as_float(w[s].x & 0xFFFF0000u))),
-                                         fmaxf(fabsf(__uint_as_float(w[s].y << 16)),
-                                               fabsf(__uint_as_float(w[s].y & 0xFFFF0000u)))));
+                    e = max(e, max(max(w[s].x & 0x7F80u, (w[s].x >> 16) & 0x7F80u),
+                                   max(w[s].y & 0x7F80u, (w[s].y >> 16) & 0x7F80u)));
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                // 2^e <= mx < 2^(e+1), e within what both 2^-e and 2^e allow
-                const int e = min(126, max(-126, (int)(__float_as_uint(mx) >> 23) - 127));
-                const float dn = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+                e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+                // the row's largest entry into [1, 2), within what 2^-x and 2^x allow; none
+                // for a row of zeros
+                const int x = e == 0 ? 0 : min(126, max(-126, (int)(e >> 7) - 127));
+                const float dn = __uint_as_float((uint32_t)(127 - x) << 23);
+                const float up = __uint_as_float((uint32_t)(127 + x) << 23);
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     qf[t][s][0] = pack<true>(__uint_as_float(w[s].x << 16) * dn,
@@ -201,118 +267,43 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
         }
         // keys below `all` are seen by every row of the tile
         const int all = a.causal ? k.i.kv - k.i.q_len + token_of(rbase, a.gqa_inv) + 1 : k.i.kv;
-        float m[NT][2], l[NT][2], o[MT][NT][4];
+        // m: reference of the weights; mp: of what O holds (e4m3: the weights times
+        // v_scale; else the same)
+        float m[NT][2], mp[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            m[t][0] = m[t][1] = -INFINITY;
+            m[t][0] = m[t][1] = mp[t][0] = mp[t][1] = -INFINITY;
             l[t][0] = l[t][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
         }
-        // ---- the warp's stages: numbers warp, warp + WARPS, ... of the run
-        const int key_first = k.u0 * kBlockTokens;
-        const int key_end = min(k.nk, k.u1 * kBlockTokens);
-        const int n_all = key_end > key_first ? (key_end - key_first + KEYS - 1) / KEYS : 0;
-        const int n = n_all > warp ? (n_all - warp + WARPS - 1) / WARPS : 0;
-        int32_t page_of = -1;                              // lane i: page of the batch's stage i
-        float ks_of = 1.f, vs_of = 1.f;
-        auto look_up = [&](int j0) {                       // 32 stages' pages and scales
-            const int j = j0 + lane;
-            page_of = -1;
-            if (j < n) {
-                const int p = (key_first + (warp + j * WARPS) * KEYS) / kBlockTokens;
-                const int64_t at = (int64_t)k.s * a.b.table_stride + p;
-                const int32_t page = a.b.page_table[at];
-                bool ok = page >= 0 && page < a.b.n_pages;
-                if (E4 && a.k_scale) {
-                    const int64_t r = a.b.scale_rows ? (int64_t)a.b.scale_rows[at] : (int64_t)page;
-                    ok = ok && r >= 0 && r < a.b.n_scale_rows;
-                    if (ok) {
-                        const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + k.g;
-                        ks_of = checked_scale(a.k_scale[so], a.b.err);
-                        vs_of = checked_scale(a.v_scale[so], a.b.err);
-                    }
-                }
-                if (ok) page_of = page;
-                else atomicOr(a.b.err, kErrBatch);
-            }
-        };
-        float ks_q[S], vs_q[S];                            // scales of the stages in flight
-        auto issue = [&](int j, int slot) {
-            if (j < n) {
-                const int32_t page = __shfl_sync(0xffffffffu, page_of, j & 31);
-                const int key0 = key_first + (warp + j * WARPS) * KEYS;
-                const int64_t head = ((int64_t)max(page, 0) * a.b.L + a.b.layer) * a.b.G + k.g;
-                const int64_t off = (head * kBlockTokens + (key0 & (kBlockTokens - 1))) * LY::ROW;
-                const char *kp = static_cast<const char *>(a.k_pages) + off;
-                const char *vp = static_cast<const char *>(a.v_pages) + off;
-                const uint32_t dst = ring32 + slot * LY::STAGE;
-                const int n_rows = page >= 0 ? k.i.kv - key0 : 0;   // rows behind them read as 0
-#pragma unroll
-                for (int i = 0; i < LY::HALF / 512; ++i) {
-                    const int x = i * 32 + lane, row = x / CH, ch = x % CH;
-                    copy16(dst + place(row, ch), kp + x * 16, row < n_rows);
-                }
-#pragma unroll
-                for (int i = 0; i < LY::HALF / 512; ++i) {
-                    const int x = i * 32 + lane, row = x / CH, ch = x % CH;
-                    copy16(dst + LY::HALF + place(row, ch), vp + x * 16, row < n_rows);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        auto scales = [&](int j) {
-            return make_float2(__shfl_sync(0xffffffffu, ks_of, j & 31),
-                               __shfl_sync(0xffffffffu, vs_of, j & 31));
-        };
-        look_up(0);
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            if constexpr (E4) {
-                const float2 sc = scales(i);
-                ks_q[i] = sc.x;
-                vs_q[i] = sc.y;
-            }
-            issue(i, i);
-        }
         int slot = 0;
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
             __syncwarp();
-            float ks = 1.f, vs = 1.f;
+            const float ks = E4 ? ks_q[0] : 1.f, lv = E4 ? lv_q[0] : 0.f;
             {
                 // the slot that the previous stage left
                 const int jn = j + S - 1;
                 if ((jn & 31) == 0) look_up(jn);
-                const int put = slot == 0 ? S - 1 : slot - 1;
-                if constexpr (E4) {
-                    const float2 sc = scales(jn);
-                    ks = ks_q[0];
-                    vs = vs_q[0];
-#pragma unroll
-                    for (int i = 0; i + 1 < S - 1; ++i) {
-                        ks_q[i] = ks_q[i + 1];
-                        vs_q[i] = vs_q[i + 1];
-                    }
-                    ks_q[S - 2] = sc.x;
-                    vs_q[S - 2] = sc.y;
-                }
-                issue(jn, put);
+                issue(jn, slot == 0 ? S - 1 : slot - 1);
             }
-            const int key0 = key_first + (warp + j * WARPS) * KEYS;
+            const int key0 = key_first + (warp + j * kWarps) * KEYS;
             const uint32_t kb = ring32 + slot * LY::STAGE, vb = kb + LY::HALF;
             if (++slot == S) slot = 0;
 
-            // ---- scores of the stage's keys, 16 at a time
+            // ---- scores of the stage's keys, 16 at a time, in two sums each
             float s[KEYS / 16][NT][4];
 #pragma unroll
             for (int u = 0; u < KEYS / 16; ++u) {
+                float s2[2][NT][4];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[u][t][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s2[0][t][e] = s2[1][t][e] = 0.f;
                 const int row = u * 16 + (lane & 15);
                 if constexpr (!E4) {
 #pragma unroll
@@ -320,7 +311,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
                         uint32_t f[4];
                         ldm4(f, kb + place(row, 2 * x + (lane >> 4)));
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma<false>(s[u][t], f, qf[t][x][0], qf[t][x][1]);
+                        for (int t = 0; t < NT; ++t) mma<false>(s2[x & 1][t], f, qf[t][x][0], qf[t][x][1]);
                     }
                 } else {
 #pragma unroll
@@ -330,48 +321,63 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
                         // f[0], f[1]: keys 0-7, 8-15 of chunk x; f[2], f[3]: of chunk x + 1
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint32_t fa[4] = {e4m3_f16(f[2 * y]), e4m3_f16(f[2 * y + 1]),
-                                                    e4m3_f16(f[2 * y] >> 16),
-                                                    e4m3_f16(f[2 * y + 1] >> 16)};
+                            uint32_t fa[4];
+                            e4m3_f16(f[2 * y], fa[0], fa[2]);
+                            e4m3_f16(f[2 * y + 1], fa[1], fa[3]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
-                                mma<true>(s[u][t], fa, qf[t][x + y][0], qf[t][x + y][1]);
+                                mma<true>(s2[y][t], fa, qf[t][x + y][0], qf[t][x + y][1]);
                         }
                     }
                 }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][t][e] = s2[0][t][e] + s2[1][t][e];
             }
             // ---- scaled, masked, against the running maximum
             const bool edge = key0 + KEYS > all;
             bool grow = false;
 #pragma unroll
-            for (int u = 0; u < KEYS / 16; ++u)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int b = 0; b < 2; ++b) {
+                    const float f = E4 ? cm[t][b] * ks : cm[t][b];
+                    float top = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = s[u][t][e] * (E4 ? cm[t][e & 1] * ks : cm[t][e & 1]);
-                        if (edge && key0 + u * 16 + g8 + (e >> 1) * 8 >= vis[t][e & 1]) x = -INFINITY;
-                        s[u][t][e] = x;
-                        grow |= x > m[t][e & 1] + kMoveMax || (m[t][e & 1] == -INFINITY && x > -INFINITY);
-                    }
+                    for (int u = 0; u < KEYS / 16; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x = s[u][t][2 * h + b] * f;
+                            if (edge && key0 + u * 16 + g8 + h * 8 >= vis[t][b]) x = -INFINITY;
+                            s[u][t][2 * h + b] = x;
+                            top = fmaxf(top, x);
+                        }
+                    // (a first finite score exceeds the m of -infinity)
+                    grow |= top > m[t][b] + kMoveMax || (E4 && top + lv > mp[t][b] + kMoveMax);
+                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        float x = m[t][b];
+                        float x = -INFINITY;
 #pragma unroll
                         for (int u = 0; u < KEYS / 16; ++u) x = fmaxf(x, fmaxf(s[u][t][b], s[u][t][b + 2]));
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                        const float f = m[t][b] == -INFINITY ? 0.f : ex2(m[t][b] - x);
-                        m[t][b] = x;
+                        const float mn = fmaxf(m[t][b], x), mpn = E4 ? fmaxf(mp[t][b], x + lv) : mn;
+                        const bool none = m[t][b] == -INFINITY;
+                        const float f = none ? 0.f : ex2(m[t][b] - mn);
+                        const float fp = E4 ? (none ? 0.f : ex2(mp[t][b] - mpn)) : f;
+                        m[t][b] = mn;
+                        mp[t][b] = mpn;
                         l[t][b] *= f;
 #pragma unroll
                         for (int i = 0; i < MT; ++i) {
-                            o[i][t][b] *= f;
-                            o[i][t][b + 2] *= f;
+                            o[i][t][b] *= fp;
+                            o[i][t][b + 2] *= fp;
                         }
                     }
             }
@@ -379,22 +385,28 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
             uint32_t pf[KEYS / 16][NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0];
-                const float b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                float base[2], w[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    base[b] = m[t][b] == -INFINITY ? 0.f : m[t][b];
+                    w[b] = !E4 ? 1.f : m[t][b] == -INFINITY ? 0.f : ex2(lv + m[t][b] - mp[t][b]);
+                }
 #pragma unroll
                 for (int u = 0; u < KEYS / 16; ++u) {
                     float p[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) p[e] = ex2(s[u][t][e] - (e & 1 ? b1 : b0));
-                    l[t][0] += p[0] + p[2];
-                    l[t][1] += p[1] + p[3];
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2(s[u][t][e] - base[e & 1]);
+                        l[t][e & 1] += p[e];
+                        if (E4) p[e] *= w[e & 1];
+                    }
                     pf[u][t][0] = transposed(pack<E4>(p[0], p[1]));
                     pf[u][t][1] = transposed(pack<E4>(p[2], p[3]));
                 }
             }
-            if constexpr (!E4) {
 #pragma unroll
-                for (int u = 0; u < KEYS / 16; ++u) {
+            for (int u = 0; u < KEYS / 16; ++u) {
+                if constexpr (!E4) {
                     const int row = u * 16 + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
@@ -403,152 +415,164 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) mma<false>(o[i][t], f, pf[u][t][0], pf[u][t][1]);
                     }
-                }
-            } else {
+                } else {
+                    const int row = u * 16 + (lane & 15);
 #pragma unroll
-                for (int i = 0; i < MT; i += 2) {
-                    float po[2][NT][4];
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) po[y][t][e] = 0.f;
-#pragma unroll
-                    for (int u = 0; u < KEYS / 16; ++u) {
-                        const int row = u * 16 + (lane & 15);
+                    for (int i = 0; i < MT; i += 2) {
                         uint32_t f[4];
                         ldm4t(f, vb + place(row, i + (lane >> 4)));
                         // f[0], f[1]: keys 0-7, 8-15 of chunk i; a register holds two keys'
                         // two adjacent d: the even d's are rows 0-7, the odd ones 8-15
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const uint32_t lo = __byte_perm(f[2 * y], 0, 0x3120);
-                            const uint32_t hi = __byte_perm(f[2 * y + 1], 0, 0x3120);
-                            const uint32_t fa[4] = {e4m3_f16(lo), e4m3_f16(lo >> 16), e4m3_f16(hi),
-                                                    e4m3_f16(hi >> 16)};
+                            uint32_t fa[4];
+                            e4m3_f16(__byte_perm(f[2 * y], 0, 0x3120), fa[0], fa[1]);
+                            e4m3_f16(__byte_perm(f[2 * y + 1], 0, 0x3120), fa[2], fa[3]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
-                                mma<true>(po[y][t], fa, pf[u][t][0], pf[u][t][1]);
+                                mma<true>(o[i + y][t], fa, pf[u][t][0], pf[u][t][1]);
                         }
                     }
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[i + y][t][e] += vs * po[y][t][e];
                 }
             }
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         // ---- the warps' sums, joined through shared memory (the ring is idle)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
-                    l[t][b] += __shfl_xor_sync(0xffffffffu, l[t][b], off);
         __syncthreads();
         float *rec = reinterpret_cast<float *>(smem) + warp * LY::REC;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
+            for (int b = 0; b < 2; ++b) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int d = E4 ? i * 16 + 2 * g8 + (e >> 1) : i * 16 + g8 + (e >> 1) * 8;
-                    rec[(t * 8 + c4 * 2 + (e & 1)) * LY::ORS + d] = o[i][t][e];
+                for (int off = 4; off < 32; off <<= 1)
+                    l[t][b] += __shfl_xor_sync(0xffffffffu, l[t][b], off);
+                const int r = t * 8 + c4 * 2 + b;
+                const float f = E4 && m[t][b] != -INFINITY ? ex2(mp[t][b] - m[t][b]) : 1.f;
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        rec[r * LY::ORS + i * 16 + (E4 ? 2 * g8 + h : g8 + 8 * h)] = o[i][t][2 * h + b] * f;
+                if (g8 == 0) {
+                    rec[RB * LY::ORS + r] = m[t][b];
+                    rec[RB * LY::ORS + RB + r] = l[t][b];
                 }
-            if (g8 == 0)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    rec[RB * LY::ORS + t * 8 + c4 * 2 + b] = m[t][b];
-                    rec[RB * LY::ORS + RB + t * 8 + c4 * 2 + b] = l[t][b];
-                }
-        }
-        __syncthreads();
+            }
         const bool whole = k.whole();
         const int c0 = whole ? cta : k.first_cta(), c1 = whole ? cta : k.last_cta();
         constexpr size_t PREC = (size_t)RB * (D + 2);
-        float *part = a.part + part_slot(cta, cta == c0) * PREC;
-        const float *all_rec = reinterpret_cast<const float *>(smem);
-        auto put = [&](int r, int q, float4 v, float mm, float ll) {   // the finished row's quad q
-            const int row = rbase + r, tok = token_of(row, a.gqa_inv), h = k.g * a.gqa + row - tok * a.gqa;
-            const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) +
-                                 (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D + q * 4;
-            *reinterpret_cast<uint2 *>(dst) =
-                make_uint2(pack<false>(v.x * inv, v.y * inv), pack<false>(v.z * inv, v.w * inv));
-            if (q == 0 && a.lse)
-                a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] =
-                    mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(ll);
-        };
-        for (int x = tid; x < rows * (D / 4); x += WARPS * 32) {
-            const int r = x / (D / 4), q = x % (D / 4);
-            float mm = -INFINITY;
+        constexpr int QUADS = D / 4;
+        for (bool final = whole;; final = true) {
+            // the four warps' sums of a row quad; to the output, or to this CTA's part
+            __syncthreads();
+#pragma unroll 1
+            for (int x = tid; x < rows * QUADS; x += kWarps * 32) {
+                const int r = x / QUADS, q = x % QUADS;
+                const float *all_rec = reinterpret_cast<const float *>(smem);
+                float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, all_rec[w * LY::REC + RB * LY::ORS + r]);
-            const float base = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, all_rec[w * LY::REC + RB * LY::ORS + r]);
+                const float base = mm == -INFINITY ? 0.f : mm;
+                float ll = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                const float *rc = all_rec + w * LY::REC;
-                const float f = ex2(rc[RB * LY::ORS + r] - base);
-                ll += f * rc[RB * LY::ORS + RB + r];
-                const float4 y = *reinterpret_cast<const float4 *>(rc + r * LY::ORS + q * 4);
-                v.x += f * y.x;
-                v.y += f * y.y;
-                v.z += f * y.z;
-                v.w += f * y.w;
-            }
-            if (whole) {
-                put(r, q, v, mm, ll);
-            } else {
-                *reinterpret_cast<float4 *>(part + r * D + q * 4) = v;
-                if (q == 0) {
-                    part[RB * D + r] = mm;
-                    part[RB * D + RB + r] = ll;
+                for (int w = 0; w < kWarps; ++w) {
+                    const float *rc = all_rec + w * LY::REC;
+                    const float f = ex2(rc[RB * LY::ORS + r] - base);
+                    ll += f * rc[RB * LY::ORS + RB + r];
+                    const float4 y = *reinterpret_cast<const float4 *>(rc + r * LY::ORS + q * 4);
+                    v.x += f * y.x;
+                    v.y += f * y.y;
+                    v.z += f * y.z;
+                    v.w += f * y.w;
+                }
+                if (final) {
+                    const int row = rbase + r, tok = token_of(row, a.gqa_inv);
+                    const int h = k.g * a.gqa + row - tok * a.gqa;
+                    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                               (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D +
+                                               q * 4) =
+                        make_uint2(pack<false>(v.x * inv, v.y * inv), pack<false>(v.z * inv, v.w * inv));
+                    if (q == 0 && a.lse)
+                        a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] =
+                            mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(ll);
+                } else {
+                    float *part = a.part + part_slot(cta, cta == c0) * PREC;
+                    *reinterpret_cast<float4 *>(part + r * D + q * 4) = v;
+                    if (q == 0) {
+                        part[RB * D + r] = mm;
+                        part[RB * D + RB + r] = ll;
+                    }
                 }
             }
-        }
-        if (!whole) {
-            // the last CTA of the tile to leave its sums joins them, in CTA order
-            __threadfence();
-            __syncthreads();
+            __syncthreads();                               // the records are free
+            if (final) break;
+            // the last CTA of the tile to leave its part joins them: warp w takes parts
+            // w, w + 4, ... in order, a lane a column quad of every row, so that the
+            // loads of whole parts are in flight together; then the warps' sums as before
             if (tid == 0) {
+                __threadfence();                           // the whole CTA's part, met at the barrier
                 is_last = atomicAdd(a.count + c0, 1) == c1 - c0;
                 if (is_last) a.count[c0] = 0;              // ready for the next call
                 __threadfence();
             }
             __syncthreads();
-            if (is_last) {
-                for (int x = tid; x < rows * (D / 4); x += WARPS * 32) {
-                    const int r = x / (D / 4), q = x % (D / 4);
-                    float mm = -INFINITY;
-                    for (int p = c0; p <= c1; ++p)
-                        mm = fmaxf(mm, __ldcg(a.part + part_slot(p, p == c0) * PREC + RB * D + r));
-                    const float base = mm == -INFINITY ? 0.f : mm;
-                    float ll = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int p = c0; p <= c1; ++p) {
-                        const float *rc = a.part + part_slot(p, p == c0) * PREC;
-                        const float f = ex2(__ldcg(rc + RB * D + r) - base);
-                        ll += f * __ldcg(rc + RB * D + RB + r);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(rc + r * D + q * 4));
-                        v.x += f * y.x;
-                        v.y += f * y.y;
-                        v.z += f * y.z;
-                        v.w += f * y.w;
+            if (!is_last) break;
+            constexpr int RPL = RB * QUADS / 32;           // (row, quad)s of a lane
+            constexpr int Y = RPL <= 8 ? 2 : 1;            // parts at a time
+            float jm[RPL], jl[RPL];
+            float4 jo[RPL];
+            const int q = lane % QUADS, r0 = lane / QUADS;
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                jm[i] = -INFINITY;
+                jl[i] = 0.f;
+                jo[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll 1
+            for (int p = c0 + warp; p <= c1; p += Y * kWarps) {
+                float pm[Y][RPL], pl[Y][RPL];
+                float4 v[Y][RPL];
+#pragma unroll
+                for (int y = 0; y < Y; ++y) {
+                    const int pp = min(p + y * kWarps, c1);
+                    const float *rc = a.part + part_slot(pp, pp == c0) * PREC;
+#pragma unroll
+                    for (int i = 0; i < RPL; ++i) {
+                        const int r = min(r0 + i * (32 / QUADS), rows - 1);
+                        pm[y][i] = __ldcg(rc + RB * D + r);
+                        pl[y][i] = __ldcg(rc + RB * D + RB + r);
+                        v[y][i] = __ldcg(reinterpret_cast<const float4 *>(rc + r * D) + q);
                     }
-                    put(r, q, v, mm, ll);
+                }
+#pragma unroll
+                for (int y = 0; y < Y; ++y) {
+                    if (p + y * kWarps > c1) continue;
+#pragma unroll
+                    for (int i = 0; i < RPL; ++i) {
+                        const float mm = fmaxf(jm[i], pm[y][i]), base = mm == -INFINITY ? 0.f : mm;
+                        const float f = ex2(jm[i] - base), w = ex2(pm[y][i] - base);
+                        jm[i] = mm;
+                        jl[i] = jl[i] * f + pl[y][i] * w;
+                        jo[i].x = jo[i].x * f + v[y][i].x * w;
+                        jo[i].y = jo[i].y * f + v[y][i].y * w;
+                        jo[i].z = jo[i].z * f + v[y][i].z * w;
+                        jo[i].w = jo[i].w * f + v[y][i].w * w;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RPL; ++i) {
+                const int r = r0 + i * (32 / QUADS);
+                *reinterpret_cast<float4 *>(rec + r * LY::ORS + q * 4) = jo[i];
+                if (q == 0) {
+                    rec[RB * LY::ORS + r] = jm[i];
+                    rec[RB * LY::ORS + RB + r] = jl[i];
                 }
             }
         }
-        __syncthreads();                                   // the ring is free for the next segment
     } while (k.next(a));
 }
 
@@ -556,14 +580,13 @@ namespace {
 
 template <int D, bool E4, int NT>
 cudaError_t decode_t(const AttendArgs &a, cudaStream_t s) {
-    constexpr int WARPS = 4;
-    using LY = Lay<D, E4, NT, WARPS>;
-    auto kern = attend_decode_kernel<D, E4, NT, WARPS>;
+    using LY = Lay<D, E4, NT>;
+    auto kern = attend_decode_kernel<D, E4, NT>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
-    const int ctas = min(kAttendMaxCtas, 2 * sm_count());
-    kern<<<ctas, WARPS * 32, LY::SMEM, s>>>(a, 8);
+    const int ctas = min(kAttendMaxCtas, LY::CTAS * sm_count());
+    kern<<<ctas, kWarps * 32, LY::SMEM, s>>>(a, kMinPages);
     note_launch();
     return cudaGetLastError();
 }
