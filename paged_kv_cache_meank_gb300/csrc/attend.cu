@@ -32,7 +32,7 @@ struct Lay {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = RB * D;
     static constexpr int FLOATS = OFF_P + NBUF * PAGE;
-    static constexpr int SMEM = FLOATS * 4 + (kMaxSeqs + 1) * 4;
+    static constexpr int SMEM = FLOATS * 4 + kPreInts * 4;
 };
 
 }  // namespace
@@ -56,7 +56,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
     }
     __syncthreads();
     W k;
-    if (!k.start(a, pre, line, cta, gridDim.x, min_units)) return;
+    if (!k.start(a, pre, line, cta)) return;
     const int row0 = KS ? 0 : warp * kRows;     // the warp's rows of the tile
     float *kb = sm + LY::OFF_P + (KS ? warp * LY::PAGE : 0), *vb = kb + kBlockTokens * LY::KST;
     do {

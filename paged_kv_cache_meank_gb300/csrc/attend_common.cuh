@@ -48,6 +48,7 @@ struct LineInfo {
     int total;     // units of all
     int most;      // the largest row tile's
     int pad;       // units every row tile is counted as, or 0: its own
+    int per;       // units of one CTA's run
 };
 
 template <int RB, int UNIT>
@@ -64,59 +65,57 @@ struct Line {
     __host__ __device__ static __forceinline__ int weight(const SeqInfo &i, const AttendArgs &a, int r) {
         return max(1, (keys(i, a, r) + UNIT - 1) / UNIT);
     }
-    // Lays the line out: pre[s] = units of the sequences before s (pre: kMaxSeqs
-    // + 1 in shared memory).  By one warp, a lane to a sequence.
+    // Lays the line out: pre[s] = units of the sequences before s, or with `pad`
+    // their row tiles (pre: kMaxSeqs + 1 in shared memory).  By one warp, a lane to a
+    // sequence.
     template <bool PAD>
     __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units) {
         const int lane = threadIdx.x & 31;
-        LineInfo li{0, 1, 0};
-        for (int pass = 0; pass < 2; ++pass) {
-            int run = 0, items = 0;
+        LineInfo li{0, 1, 0, 0};
+        int items = 0;
 #pragma unroll 1
-            for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
-                const int s = s0 + lane;
-                int w = 0, n = 0;
-                if (s < a.b.n_seqs) {
-                    bool ok;
-                    const SeqInfo i = seq_info(a.b, s, &ok);
-                    if (!ok) atomicOr(a.b.err, kErrBatch);
-                    n = tiles(i, a);
-                    if (pass) {
-                        w = n * li.pad;
-                    } else {
+        for (int s0 = 0; s0 < a.b.n_seqs; s0 += 32) {
+            const int s = s0 + lane;
+            int w = 0, n = 0;
+            if (s < a.b.n_seqs) {
+                bool ok;
+                const SeqInfo i = seq_info(a.b, s, &ok);
+                if (!ok) atomicOr(a.b.err, kErrBatch);
+                n = tiles(i, a);
 #pragma unroll 1
-                        for (int r = 0; r < n; ++r) {
-                            const int x = weight(i, a, r);
-                            w += x;
-                            li.most = max(li.most, x);
-                        }
+                for (int r = 0; r < n; ++r) {
+                    const int x = weight(i, a, r);
+                    w += x;
+                    li.most = max(li.most, x);
+                }
+            }
+            w *= a.b.G;
+            n *= a.b.G;
+            int last = 0;
+            if (a.b.n_seqs > 1) {
+                last = 31;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, w, o);
+                    const int un = __shfl_up_sync(0xffffffffu, n, o);
+                    if (lane >= o) {
+                        w += up;
+                        n += un;
                     }
                 }
-                w *= a.b.G;
-                n *= a.b.G;
-                if (a.b.n_seqs > 1) {
-#pragma unroll 1
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int up = __shfl_up_sync(0xffffffffu, w, o);
-                        const int un = __shfl_up_sync(0xffffffffu, n, o);
-                        if (lane >= o) {
-                            w += up;
-                            n += un;
-                        }
-                    }
-                }
-                if (s < a.b.n_seqs) pre[s + 1] = run + w;
-                const int last = a.b.n_seqs > 1 ? 31 : 0;
-                run += __shfl_sync(0xffffffffu, w, last);
-                items += __shfl_sync(0xffffffffu, n, last);
             }
-            li.total = run;
-            if (pass == 0) {
-                li.most = __reduce_max_sync(0xffffffffu, li.most);
-                if (!PAD || (li.pad = padded_weight(items, li, n_ctas, min_units)) == 0) break;
+            if (s < a.b.n_seqs) {
+                pre[s + 1] = li.total + w;
+                if (PAD) pre[kMaxSeqs + 1 + s + 1] = items + n;
             }
+            li.total += __shfl_sync(0xffffffffu, w, last);
+            items += __shfl_sync(0xffffffffu, n, last);
         }
-        if (lane == 0) pre[0] = 0;
+        if (lane == 0) pre[0] = pre[kMaxSeqs + 1] = 0;
+        li.most = __reduce_max_sync(0xffffffffu, li.most);
+        if (PAD) li.pad = padded_weight(items, li, n_ctas, min_units);
+        if (li.pad) li.total = items * li.pad;
+        li.per = run_units(li, items, n_ctas, min_units);
         __syncwarp();
         return li;
     }
@@ -137,28 +136,28 @@ struct Line {
                    ? pad
                    : 0;
     }
+    // Units of one CTA's run: an equal share, but not so small that a tile's join
+    // costs more than its keys, unless whole tiles are smaller.  Of tiles counted
+    // alike, a CTA takes an equal part of one, or with more tiles than CTAs a
+    // multiple of a whole, a half, a third or a quarter: the first of these that
+    // gives away at most 1/16 of the share, else the one that gives away least.
+    __host__ __device__ static int run_units(const LineInfo &li, int items, int n_ctas, int min_units) {
+        const int least = min(li.most, min_units);
+        if (li.pad && items * 4 < n_ctas * 3) return li.pad / min(n_ctas / items, li.most / least);
+        const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
+        if (!li.pad) return max(share, least);
+        int best = 0;
+#pragma unroll 1
+        for (int m = 1; m <= 4; ++m) {
+            const int part = li.pad / m, run = (share + part - 1) / part * part;
+            if (best == 0 || run < best) best = run;
+            if (run - share <= share / 16) return run;
+        }
+        return best;
+    }
 };
 
-// Units of one CTA's run: an equal share, but not so small that a tile's join
-// costs more than its keys, unless whole tiles are smaller.  Of tiles counted
-// alike, a CTA takes an equal part of one, or with more tiles than CTAs a
-// multiple of a whole, a half, a third or a quarter: the first of these that
-// gives away at most 1/16 of the share, else the one that gives away least.
-__host__ __device__ __forceinline__ int run_units(const LineInfo &li, int n_ctas, int min_units) {
-    const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
-    const int least = min(li.most, min_units);
-    if (!li.pad) return max(share, least);
-    const int items = li.total / li.pad;
-    if (items * 4 < n_ctas * 3) return li.pad / min(n_ctas / items, li.most / least);
-    int best = 0;
-#pragma unroll 1
-    for (int m = 1; m <= 4; ++m) {
-        const int part = li.pad / m, run = (share + part - 1) / part * part;
-        if (best == 0 || run < best) best = run;
-        if (run - share <= share / 16) return run;
-    }
-    return best;
-}
+constexpr int kPreInts = 2 * (kMaxSeqs + 1);   // shared memory of lay_out
 
 // A walk over one CTA's run of the line.
 template <int RB, int UNIT>
@@ -172,30 +171,34 @@ struct Walk {
 
     // False when the CTA's run is empty.
     __host__ __device__ __forceinline__ bool start(const AttendArgs &a, const int *pre, const LineInfo &li,
-                                                   int cta, int n_ctas, int min_units) {
-        per = run_units(li, n_ctas, min_units);
+                                                   int cta) {
+        per = li.per;
         if ((int64_t)cta * per >= li.total) return false;
         x = cta * per;
         end = li.total - x < per ? li.total : x + per;
-        int lo = 0, hi = a.b.n_seqs - 1;                // the last s with pre[s] <= x
+        pad = li.pad;
+        const int unit = pad ? pad : 1;
+        if (pad) pre += kMaxSeqs + 1;                   // in row tiles
+        int lo = 0, hi = a.b.n_seqs - 1;                // the last s with pre[s] * unit <= x
         while (lo < hi) {
             const int m = (lo + hi + 1) >> 1;
-            if (pre[m] <= x) lo = m; else hi = m - 1;
+            if (pre[m] * unit <= x) lo = m; else hi = m - 1;
         }
         s = lo;
-        pad = li.pad;
         bool ok;
         i = seq_info(a.b, s, &ok);
         n_tiles = LN::tiles(i, a);
-        int rem = x - pre[s];
-        const int per_head = (pre[s + 1] - pre[s]) / a.b.G;
+        int rem = x - pre[s] * unit;
+        const int per_head = pad ? n_tiles * pad : (pre[s + 1] - pre[s]) / a.b.G;
         g = rem / per_head;
         rem -= g * per_head;
+        r = 0;
         if (pad) {
-            r = rem / pad;
-            rem -= r * pad;
+            if (n_tiles > 1) {
+                r = rem / pad;
+                rem -= r * pad;
+            }
         } else {
-            r = 0;
             for (int y = LN::weight(i, a, 0); rem >= y; y = LN::weight(i, a, r)) {
                 rem -= y;
                 ++r;

@@ -20,9 +20,7 @@
 // a power of two per row, the page's k_scale goes into the factor of the scores
 // and the weights times v_scale have a running maximum of their own.
 //
-// Rows of 256 bytes (bf16, d = 128): two CTAs an SM with three 8 KB stages a
-// warp.  Narrower rows carry more arithmetic for their bytes: three CTAs with
-// four 4 KB stages a warp.
+// Two or three CTAs an SM, with three 8 KB or four 4 KB stages a warp.
 #include <math.h>
 
 #include "attend_common.cuh"
@@ -40,7 +38,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 constexpr int kMinPages = 8;               // of a CTA's run: below, a join costs more than the keys
 
-template <int D, bool E4, int NT>
+template <int D, bool E4, int NT, int CTAS>
 struct Lay {
     static constexpr int RB = 8 * NT;
     static constexpr int ROW = E4 ? D : 2 * D;             // bytes of a K or V row
@@ -48,12 +46,11 @@ struct Lay {
     static constexpr int HALF = KEYS * ROW;                // K (or V) of a stage
     static constexpr int STAGE = 2 * HALF;
     static constexpr int STAGES = STAGE == 8192 ? 3 : 4;
-    static constexpr int CTAS = NT == 1 && ROW < 256 ? 3 : 2;   // of an SM
     static constexpr int RING = STAGES * STAGE;            // of one warp
     static constexpr int ORS = D + 4;                      // a row of a warp's sums
     static constexpr int REC = RB * ORS + 2 * RB;          // floats: o, m, l
     static constexpr int BYTES = kWarps * (RING > REC * 4 ? RING : REC * 4);
-    static constexpr int SMEM = BYTES + (kMaxSeqs + 1) * 4;
+    static constexpr int SMEM = BYTES + kPreInts * 4;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -116,10 +113,10 @@ __device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t &lo, uint32_t &hi)
 
 }  // namespace
 
-template <int D, bool E4, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Lay<D, E4, NT>::CTAS)
+template <int D, bool E4, int NT, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS)
 attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
-    using LY = Lay<D, E4, NT>;
+    using LY = Lay<D, E4, NT, CTAS>;
     constexpr int RB = LY::RB, KS = D / 16, MT = D / 16, KEYS = LY::KEYS, S = LY::STAGES;
     constexpr int CH = LY::ROW / 16;                       // 16-byte chunks of a row
     using W = Walk<RB, kBlockTokens>;
@@ -136,7 +133,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     }
     __syncthreads();
     W k;
-    if (!k.start(a, pre, line, cta, gridDim.x, min_units)) return;
+    if (!k.start(a, pre, line, cta)) return;
     const uint32_t ring32 = tc::smem_u32(smem + warp * LY::RING);
     const float c = a.scale * kLog2e;
     // a chunk's place in its row: the 8 rows that an ldmatrix phase reads at one
@@ -578,14 +575,14 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
 
 namespace {
 
-template <int D, bool E4, int NT>
+template <int D, bool E4, int NT, int CTAS>
 cudaError_t decode_t(const AttendArgs &a, cudaStream_t s) {
-    using LY = Lay<D, E4, NT>;
-    auto kern = attend_decode_kernel<D, E4, NT>;
+    using LY = Lay<D, E4, NT, CTAS>;
+    auto kern = attend_decode_kernel<D, E4, NT, CTAS>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
-    const int ctas = min(kAttendMaxCtas, LY::CTAS * sm_count());
+    const int ctas = min(kAttendMaxCtas, CTAS * sm_count());
     kern<<<ctas, kWarps * 32, LY::SMEM, s>>>(a, kMinPages);
     note_launch();
     return cudaGetLastError();
@@ -593,7 +590,13 @@ cudaError_t decode_t(const AttendArgs &a, cudaStream_t s) {
 
 template <int D, bool E4>
 cudaError_t decode_n(const AttendArgs &a, cudaStream_t s) {
-    return (int64_t)a.b.max_q_len * a.gqa <= 8 ? decode_t<D, E4, 1>(a, s) : decode_t<D, E4, 2>(a, s);
+    if ((int64_t)a.b.max_q_len * a.gqa > 8) return decode_t<D, E4, 2, 2>(a, s);
+    // Narrow rows carry more arithmetic for their bytes, and a third CTA hides more of
+    // it: 24 ragged sequences of e4m3 pages took 94.6 us against 101.3 with two.  One
+    // sequence, whose tiles are cut for the CTAs to share, took 40.3 against 34.5: more
+    // parts to join.
+    if ((E4 || D == 64) && (int64_t)a.b.n_seqs * a.b.G >= sm_count()) return decode_t<D, E4, 1, 3>(a, s);
+    return decode_t<D, E4, 1, 2>(a, s);
 }
 
 }  // namespace

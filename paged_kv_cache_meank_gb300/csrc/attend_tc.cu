@@ -74,7 +74,7 @@ struct Lay {
     static constexpr int OFF_BAR = OFF_QP + (E4 ? Q_TILES * TR * 4 : 0);
     static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
-    static_assert(SLOTS * TILE >= (kMaxSeqs + 1) * 4, "prefix fits the ring");
+    static_assert(SLOTS * TILE >= kPreInts * 4, "prefix fits the ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -533,7 +533,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             int *pre = reinterpret_cast<int *>(kvs);
             const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
             W k;
-            bool any = k.start(a, pre, li, blockIdx.x, gridDim.x, min_units);
+            bool any = k.start(a, pre, li, blockIdx.x);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
