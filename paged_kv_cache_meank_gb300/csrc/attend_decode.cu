@@ -3,7 +3,7 @@
 // head.  The cache is read once and each byte of it meets 16 rows at most, so
 // the kernel is bound by HBM; what counts is loads in flight.
 //
-// A warp owns every fourth stage of its CTA's run of keys (16 or 32 keys of K
+// A warp owns every fourth (or eighth) stage of its CTA's run of keys (16 or 32 keys of K
 // and V, 4-8 KB) with a ring of cp.async stages of its own in shared memory, its
 // own running maximum, weight and output, and no barrier until the run's end.
 // Keys take the 16-row side of mma.m16n8k16 and query rows the 8-column side, so
@@ -20,7 +20,13 @@
 // a power of two per row, the page's k_scale goes into the factor of the scores
 // and the weights times v_scale have a running maximum of their own.
 //
-// Two or three CTAs an SM, with three 8 KB or four 4 KB stages a warp.
+// Three 8 KB or four 4 KB stages a warp; eight to twelve warps an SM.  With fewer
+// tiles than SMs they are one CTA, for as few parts to join as can be: one
+// sequence of 32768 bf16 keys (134 MB) took 27.4 us against 31.4 with two CTAs of
+// four warps, of 65536 e4m3 keys 29.1 against 33.5.  With more, two or three CTAs,
+// so that one streams while another joins; the third where rows are narrow and carry
+// more arithmetic for their bytes (24 ragged sequences of e4m3 pages: 94.6 us against
+// 101.3 with two).
 #include <math.h>
 
 #include "attend_common.cuh"
@@ -35,10 +41,10 @@ constexpr float kMoveMax = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kWarps = 4;
 constexpr int kMinPages = 8;               // of a CTA's run: below, a join costs more than the keys
 
-template <int D, bool E4, int NT, int CTAS>
+// W warps a CTA, CTAS of them an SM.
+template <int D, bool E4, int NT, int W, int CTAS>
 struct Lay {
     static constexpr int RB = 8 * NT;
     static constexpr int ROW = E4 ? D : 2 * D;             // bytes of a K or V row
@@ -49,7 +55,10 @@ struct Lay {
     static constexpr int RING = STAGES * STAGE;            // of one warp
     static constexpr int ORS = D + 4;                      // a row of a warp's sums
     static constexpr int REC = RB * ORS + 2 * RB;          // floats: o, m, l
-    static constexpr int BYTES = kWarps * (RING > REC * 4 ? RING : REC * 4);
+    static constexpr int BYTES = W * (RING > REC * 4 ? RING : REC * 4);
+    static constexpr int MAX_CTAS = CTAS * kTileMaxCtas;
+    static constexpr int WEIGHTS = MAX_CTAS * RB * 4;      // bytes: of the parts of a join
+    static_assert(MAX_CTAS <= kAttendMaxCtas, "counts and parts are for so many");
     static constexpr int SMEM = BYTES + kPreInts * 4;
 };
 
@@ -113,16 +122,17 @@ __device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t &lo, uint32_t &hi)
 
 }  // namespace
 
-template <int D, bool E4, int NT, int CTAS>
-__global__ void __launch_bounds__(kWarps * 32, CTAS)
+template <int D, bool E4, int NT, int WARPS, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS)
 attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
-    using LY = Lay<D, E4, NT, CTAS>;
+    using LY = Lay<D, E4, NT, WARPS, CTAS>;
     constexpr int RB = LY::RB, KS = D / 16, MT = D / 16, KEYS = LY::KEYS, S = LY::STAGES;
     constexpr int CH = LY::ROW / 16;                       // 16-byte chunks of a row
     using W = Walk<RB, kBlockTokens>;
     extern __shared__ __align__(1024) uint8_t smem[];
     int *pre = reinterpret_cast<int *>(smem + LY::BYTES);
     __shared__ int is_last;
+    __shared__ float part_m[WARPS][RB], part_l[WARPS][RB];
     __shared__ LineInfo line;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
@@ -145,18 +155,21 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     do {
         const int rows_all = k.i.q_len * a.gqa, rbase = k.r * RB;
         const int rows = min(RB, rows_all - rbase);
-        // ---- the warp's stages: numbers warp, warp + kWarps, ... of the run
+        // ---- the warp's stages: numbers warp, warp + WARPS, ... of the run
         const int key_first = k.u0 * kBlockTokens;
         const int key_end = min(k.nk, k.u1 * kBlockTokens);
         const int n_all = key_end > key_first ? (key_end - key_first + KEYS - 1) / KEYS : 0;
-        const int n = n_all > warp ? (n_all - warp + kWarps - 1) / kWarps : 0;
-        int32_t page_of = -1;                              // lane i: page of the batch's stage i
+        const int n = n_all > warp ? (n_all - warp + WARPS - 1) / WARPS : 0;
+        // lane i: page and scales of the warp's stage w0 + i
+        int w0 = 0;
+        int32_t page_of = -1;
         float ks_of = 1.f, vs_of = 1.f;
-        auto look_up = [&](int j0) {                       // 32 stages' pages and scales
+        auto look_up = [&](int j0) {
+            w0 = j0;
             const int j = j0 + lane;
             page_of = -1;
             if (j < n) {
-                const int p = (key_first + (warp + j * kWarps) * KEYS) / kBlockTokens;
+                const int p = (key_first + (warp + j * WARPS) * KEYS) / kBlockTokens;
                 const int64_t at = (int64_t)k.s * a.b.table_stride + p;
                 const int32_t page = a.b.page_table[at];
                 bool ok = page >= 0 && page < a.b.n_pages;
@@ -165,19 +178,25 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
                     ok = ok && r >= 0 && r < a.b.n_scale_rows;
                     if (ok) {
                         const size_t so = ((size_t)r * a.b.L + a.b.layer) * a.b.G + k.g;
-                        ks_of = checked_scale(a.k_scale[so], a.b.err);
-                        vs_of = checked_scale(a.v_scale[so], a.b.err);
+                        ks_of = a.k_scale[so];
+                        vs_of = a.v_scale[so];
                     }
                 }
                 if (ok) page_of = page;
                 else atomicOr(a.b.err, kErrBatch);
             }
         };
-        float ks_q[S - 1], lv_q[S - 1];                    // k_scale, log2 v_scale of the stages in flight
+        // apart from look_up, so that the first stages are asked for before their scales come
+        auto check_scales = [&] {
+            if (E4 && a.k_scale && page_of >= 0) {
+                ks_of = checked_scale(ks_of, a.b.err);
+                vs_of = checked_scale(vs_of, a.b.err);
+            }
+        };
         auto issue = [&](int j, int slot) {
             if (j < n) {
-                const int32_t page = __shfl_sync(0xffffffffu, page_of, j & 31);
-                const int key0 = key_first + (warp + j * kWarps) * KEYS;
+                const int32_t page = __shfl_sync(0xffffffffu, page_of, j - w0);
+                const int key0 = key_first + (warp + j * WARPS) * KEYS;
                 const int64_t head = ((int64_t)max(page, 0) * a.b.L + a.b.layer) * a.b.G + k.g;
                 const int64_t off = (head * kBlockTokens + (key0 & (kBlockTokens - 1))) * LY::ROW + lane * 16;
                 const char *kp = static_cast<const char *>(a.k_pages) + off;
@@ -192,19 +211,11 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
                 }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if constexpr (E4) {
-#pragma unroll
-                for (int i = 0; i + 1 < S - 1; ++i) {
-                    ks_q[i] = ks_q[i + 1];
-                    lv_q[i] = lv_q[i + 1];
-                }
-                ks_q[S - 2] = __shfl_sync(0xffffffffu, ks_of, j & 31);
-                lv_q[S - 2] = (float)((int)(__float_as_uint(__shfl_sync(0xffffffffu, vs_of, j & 31)) >> 23) - 127);
-            }
         };
         look_up(0);
 #pragma unroll 1
         for (int i = 0; i < S - 1; ++i) issue(i, i);
+        check_scales();
 
         // ---- the query rows as B fragments, and what each score is multiplied by
         uint32_t qf[NT][KS][2];
@@ -281,14 +292,21 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
         for (int j = 0; j < n; ++j) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
             __syncwarp();
-            const float ks = E4 ? ks_q[0] : 1.f, lv = E4 ? lv_q[0] : 0.f;
             {
                 // the slot that the previous stage left
                 const int jn = j + S - 1;
-                if ((jn & 31) == 0) look_up(jn);
+                if (jn - w0 == 32) {
+                    look_up(j);
+                    check_scales();
+                }
                 issue(jn, slot == 0 ? S - 1 : slot - 1);
             }
-            const int key0 = key_first + (warp + j * kWarps) * KEYS;
+            float ks = 1.f, lv = 0.f;                      // k_scale, log2 v_scale of the stage
+            if constexpr (E4) {
+                ks = __shfl_sync(0xffffffffu, ks_of, j - w0);
+                lv = (float)((int)(__float_as_uint(__shfl_sync(0xffffffffu, vs_of, j - w0)) >> 23) - 127);
+            }
+            const int key0 = key_first + (warp + j * WARPS) * KEYS;
             const uint32_t kb = ring32 + slot * LY::STAGE, vb = kb + LY::HALF;
             if (++slot == S) slot = 0;
 
@@ -458,145 +476,187 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
             }
         const bool whole = k.whole();
         const int c0 = whole ? cta : k.first_cta(), c1 = whole ? cta : k.last_cta();
-        constexpr size_t PREC = (size_t)RB * (D + 2);
         constexpr int QUADS = D / 4;
-        for (bool final = whole;; final = true) {
-            // the four warps' sums of a row quad; to the output, or to this CTA's part
-            __syncthreads();
+        auto emit = [&](int r, int q, float4 v, float mm, float ll) {
+            const int row = rbase + r, tok = token_of(row, a.gqa_inv);
+            const int h = k.g * a.gqa + row - tok * a.gqa;
+            const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                       (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D + q * 4) =
+                make_uint2(pack<false>(v.x * inv, v.y * inv), pack<false>(v.z * inv, v.w * inv));
+            if (q == 0 && a.lse)
+                a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] =
+                    mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(ll);
+        };
+        // a part: m and l of RB rows, then the rows
+        constexpr size_t PREC = (size_t)RB * (D + 2);
+        // ---- the four warps' sums of a row quad; to the output, or to this CTA's part
+        __syncthreads();
 #pragma unroll 1
-            for (int x = tid; x < rows * QUADS; x += kWarps * 32) {
-                const int r = x / QUADS, q = x % QUADS;
-                const float *all_rec = reinterpret_cast<const float *>(smem);
-                float mm = -INFINITY;
+        for (int x = tid; x < rows * QUADS; x += WARPS * 32) {
+            const int r = x / QUADS, q = x % QUADS;
+            const float *all_rec = reinterpret_cast<const float *>(smem);
+            float mm = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, all_rec[w * LY::REC + RB * LY::ORS + r]);
-                const float base = mm == -INFINITY ? 0.f : mm;
-                float ll = 0.f;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, all_rec[w * LY::REC + RB * LY::ORS + r]);
+            const float base = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float *rc = all_rec + w * LY::REC;
-                    const float f = ex2(rc[RB * LY::ORS + r] - base);
-                    ll += f * rc[RB * LY::ORS + RB + r];
-                    const float4 y = *reinterpret_cast<const float4 *>(rc + r * LY::ORS + q * 4);
-                    v.x += f * y.x;
-                    v.y += f * y.y;
-                    v.z += f * y.z;
-                    v.w += f * y.w;
-                }
-                if (final) {
-                    const int row = rbase + r, tok = token_of(row, a.gqa_inv);
-                    const int h = k.g * a.gqa + row - tok * a.gqa;
-                    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                               (int64_t)(k.i.q0 + tok) * a.out_stride + (int64_t)h * D +
-                                               q * 4) =
-                        make_uint2(pack<false>(v.x * inv, v.y * inv), pack<false>(v.z * inv, v.w * inv));
-                    if (q == 0 && a.lse)
-                        a.lse[(int64_t)(k.i.q0 + tok) * a.H + h] =
-                            mm == -INFINITY ? -INFINITY : mm * kLn2 + logf(ll);
-                } else {
-                    float *part = a.part + part_slot(cta, cta == c0) * PREC;
-                    *reinterpret_cast<float4 *>(part + r * D + q * 4) = v;
-                    if (q == 0) {
-                        part[RB * D + r] = mm;
-                        part[RB * D + RB + r] = ll;
-                    }
-                }
+            for (int w = 0; w < WARPS; ++w) {
+                const float *rc = all_rec + w * LY::REC;
+                const float f = ex2(rc[RB * LY::ORS + r] - base);
+                ll += f * rc[RB * LY::ORS + RB + r];
+                const float4 y = *reinterpret_cast<const float4 *>(rc + r * LY::ORS + q * 4);
+                v.x += f * y.x;
+                v.y += f * y.y;
+                v.z += f * y.z;
+                v.w += f * y.w;
             }
-            __syncthreads();                               // the records are free
-            if (final) break;
-            // the last CTA of the tile to leave its part joins them: warp w takes parts
-            // w, w + 4, ... in order, a lane a column quad of every row, so that the
-            // loads of whole parts are in flight together; then the warps' sums as before
-            if (tid == 0) {
-                __threadfence();                           // the whole CTA's part, met at the barrier
-                is_last = atomicAdd(a.count + c0, 1) == c1 - c0;
-                if (is_last) a.count[c0] = 0;              // ready for the next call
-                __threadfence();
-            }
-            __syncthreads();
-            if (!is_last) break;
-            constexpr int RPL = RB * QUADS / 32;           // (row, quad)s of a lane
-            constexpr int Y = RPL <= 8 ? 2 : 1;            // parts at a time
-            float jm[RPL], jl[RPL];
-            float4 jo[RPL];
-            const int q = lane % QUADS, r0 = lane / QUADS;
-#pragma unroll
-            for (int i = 0; i < RPL; ++i) {
-                jm[i] = -INFINITY;
-                jl[i] = 0.f;
-                jo[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll 1
-            for (int p = c0 + warp; p <= c1; p += Y * kWarps) {
-                float pm[Y][RPL], pl[Y][RPL];
-                float4 v[Y][RPL];
-#pragma unroll
-                for (int y = 0; y < Y; ++y) {
-                    const int pp = min(p + y * kWarps, c1);
-                    const float *rc = a.part + part_slot(pp, pp == c0) * PREC;
-#pragma unroll
-                    for (int i = 0; i < RPL; ++i) {
-                        const int r = min(r0 + i * (32 / QUADS), rows - 1);
-                        pm[y][i] = __ldcg(rc + RB * D + r);
-                        pl[y][i] = __ldcg(rc + RB * D + RB + r);
-                        v[y][i] = __ldcg(reinterpret_cast<const float4 *>(rc + r * D) + q);
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < Y; ++y) {
-                    if (p + y * kWarps > c1) continue;
-#pragma unroll
-                    for (int i = 0; i < RPL; ++i) {
-                        const float mm = fmaxf(jm[i], pm[y][i]), base = mm == -INFINITY ? 0.f : mm;
-                        const float f = ex2(jm[i] - base), w = ex2(pm[y][i] - base);
-                        jm[i] = mm;
-                        jl[i] = jl[i] * f + pl[y][i] * w;
-                        jo[i].x = jo[i].x * f + v[y][i].x * w;
-                        jo[i].y = jo[i].y * f + v[y][i].y * w;
-                        jo[i].z = jo[i].z * f + v[y][i].z * w;
-                        jo[i].w = jo[i].w * f + v[y][i].w * w;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < RPL; ++i) {
-                const int r = r0 + i * (32 / QUADS);
-                *reinterpret_cast<float4 *>(rec + r * LY::ORS + q * 4) = jo[i];
+            if (whole) {
+                emit(r, q, v, mm, ll);
+            } else {
+                float *part = a.part + part_slot(cta, cta == c0) * PREC;
+                *reinterpret_cast<float4 *>(part + 2 * RB + r * D + q * 4) = v;
                 if (q == 0) {
-                    rec[RB * LY::ORS + r] = jm[i];
-                    rec[RB * LY::ORS + RB + r] = jl[i];
+                    part[r] = mm;
+                    part[RB + r] = ll;
                 }
             }
         }
+        __syncthreads();                                   // the records are free
+        if (whole) continue;
+        // ---- the last CTA of the tile to leave its part joins them, in the order of
+        // the CTAs.  The parts come to shared memory a batch ahead of their use, as
+        // many in flight as fit (one CTA reads up to 120 KB from L2), by loops
+        // that are short because they run once, out of a cold instruction cache.
+        if (tid == 0) {
+            int n_before;                                  // (orders the whole CTA's part, met at the barrier)
+            asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                         : "=r"(n_before)
+                         : "l"(a.count + c0)
+                         : "memory");
+            is_last = n_before == c1 - c0;
+            if (is_last) a.count[c0] = 0;                  // ready for the next call
+        }
+        __syncthreads();
+        if (!is_last) continue;
+        constexpr int T = WARPS * 32;
+        const int pq = rows * QUADS;                       // 16-byte pieces of a part's rows
+        const int cap = (LY::BYTES - LY::WEIGHTS) / 32 / pq;   // parts of a batch, two in flight
+        float *weight = reinterpret_cast<float *>(smem);   // [part][RB]
+        uint8_t *batch = smem + LY::WEIGHTS;
+        auto fetch = [&](int p0, int b) {
+            const int p1 = min(p0 + cap, c1 + 1);
+#pragma unroll 1
+            for (int p = p0 + warp; p < p1; p += WARPS) {
+                const float4 *src =
+                    reinterpret_cast<const float4 *>(a.part + part_slot(p, p == c0) * PREC + 2 * RB);
+                const uint32_t dst = tc::smem_u32(batch) + (b * cap + p - p0) * pq * 16;
+#pragma unroll 2
+                for (int x = lane; x < pq; x += 32) copy16(dst + x * 16, src + x, true);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fetch(c0, 0);
+        fetch(c0 + cap, 1);
+        // the rows' m and l over all parts, a thread to a row of every T / RB-th part
+        const int jr = tid % RB, jp = tid / RB;
+        float mine = -INFINITY, ll = 0.f;
+        if (jr < rows)
+#pragma unroll 1
+            for (int p = c0 + jp; p <= c1; p += T / RB) {
+                const float *rc = a.part + part_slot(p, p == c0) * PREC;
+                const float pm = __ldcg(rc + jr), pl = __ldcg(rc + RB + jr), mx = fmaxf(mine, pm);
+                const float base = mx == -INFINITY ? 0.f : mx;
+                weight[(p - c0) * RB + jr] = pm;
+                ll = ll * ex2(mine - base) + pl * ex2(pm - base);
+                mine = mx;
+            }
+        float mm = mine;
+#pragma unroll
+        for (int off = RB; off < 32; off <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+        if (lane < RB) part_m[warp][lane] = mm;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, part_m[w][jr]);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        if (jr < rows)
+#pragma unroll 1
+            for (int p = jp; p <= c1 - c0; p += T / RB)
+                weight[p * RB + jr] = ex2(weight[p * RB + jr] - base);
+        ll *= ex2(mine - base);
+#pragma unroll
+        for (int off = RB; off < 32; off <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, off);
+        if (lane < RB) part_l[warp][lane] = ll;
+        // the rows' weighted sums, a thread to one or two row quads
+        constexpr int PER = RB * QUADS > T ? RB * QUADS / T : 1;
+        float4 acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int b = 0;
+#pragma unroll 1
+        for (int p0 = c0; p0 <= c1; p0 += cap) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            const int np = min(cap, c1 + 1 - p0);
+            const float4 *rc = reinterpret_cast<const float4 *>(batch) + b * cap * pq;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int x = tid + i * T;
+                if (x >= pq) continue;
+                const float *w = weight + (p0 - c0) * RB + x / QUADS;
+#pragma unroll 4
+                for (int p = 0; p < np; ++p) {
+                    const float f = w[p * RB];
+                    const float4 y = rc[p * pq + x];
+                    acc[i].x += f * y.x;
+                    acc[i].y += f * y.y;
+                    acc[i].z += f * y.z;
+                    acc[i].w += f * y.w;
+                }
+            }
+            __syncthreads();
+            fetch(p0 + 2 * cap, b);
+            b ^= 1;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int x = tid + i * T, r = x / QUADS;
+            if (x >= pq) continue;
+            float m_all = -INFINITY, l_all = 0.f;
+#pragma unroll 1
+            for (int w = 0; w < WARPS; ++w) {
+                m_all = fmaxf(m_all, part_m[w][r]);
+                l_all += part_l[w][r];
+            }
+            emit(r, x % QUADS, acc[i], m_all, l_all);
+        }
+        __syncthreads();                                   // shared memory is the next tile's
     } while (k.next(a));
 }
 
 namespace {
 
-template <int D, bool E4, int NT, int CTAS>
+template <int D, bool E4, int NT, int WARPS, int CTAS>
 cudaError_t decode_t(const AttendArgs &a, cudaStream_t s) {
-    using LY = Lay<D, E4, NT, CTAS>;
-    auto kern = attend_decode_kernel<D, E4, NT, CTAS>;
+    using LY = Lay<D, E4, NT, WARPS, CTAS>;
+    auto kern = attend_decode_kernel<D, E4, NT, WARPS, CTAS>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
-    const int ctas = min(kAttendMaxCtas, CTAS * sm_count());
-    kern<<<ctas, kWarps * 32, LY::SMEM, s>>>(a, kMinPages);
+    const int ctas = min(LY::MAX_CTAS, CTAS * sm_count());
+    kern<<<ctas, WARPS * 32, LY::SMEM, s>>>(a, kMinPages);
     note_launch();
     return cudaGetLastError();
 }
 
 template <int D, bool E4>
 cudaError_t decode_n(const AttendArgs &a, cudaStream_t s) {
-    if ((int64_t)a.b.max_q_len * a.gqa > 8) return decode_t<D, E4, 2, 2>(a, s);
-    // Narrow rows carry more arithmetic for their bytes, and a third CTA hides more of
-    // it: 24 ragged sequences of e4m3 pages took 94.6 us against 101.3 with two.  One
-    // sequence, whose tiles are cut for the CTAs to share, took 40.3 against 34.5: more
-    // parts to join.
-    if ((E4 || D == 64) && (int64_t)a.b.n_seqs * a.b.G >= sm_count()) return decode_t<D, E4, 1, 3>(a, s);
-    return decode_t<D, E4, 1, 2>(a, s);
+    const bool many = (int64_t)a.b.n_seqs * a.b.G >= sm_count();
+    if ((int64_t)a.b.max_q_len * a.gqa > 8)
+        return many ? decode_t<D, E4, 2, 4, 2>(a, s) : decode_t<D, E4, 2, 8, 1>(a, s);
+    return many ? decode_t<D, E4, 1, 4, E4 || D == 64 ? 3 : 2>(a, s) : decode_t<D, E4, 1, 8, 1>(a, s);
 }
 
 }  // namespace
