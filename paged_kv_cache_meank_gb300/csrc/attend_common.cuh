@@ -119,6 +119,11 @@ struct Line {
         __syncwarp();
         return li;
     }
+    // The shortest run: below min_units a tile's join costs more than its keys, and a
+    // tile of twice that is not cut.
+    __host__ __device__ static int least_units(const LineInfo &li, int min_units) {
+        return li.most <= 2 * min_units ? li.most : min_units;
+    }
     // Where the row tiles are about equally long, they are all counted as `pad`
     // units, at least the longest one's: runs then begin and end at the same few
     // places of every tile (run_units).  A CTA meets one tile and not the ends of
@@ -127,7 +132,7 @@ struct Line {
     __host__ __device__ static int padded_weight(int items, const LineInfo &li, int n_ctas, int min_units) {
         if (items == 0 || (float)li.total < 0.85f * (float)items * (float)li.most) return 0;
         if (items * 4 < n_ctas * 3) {                    // several CTAs to a tile
-            const int parts = min(n_ctas / items, li.most / min(li.most, min_units));
+            const int parts = min(n_ctas / items, li.most / least_units(li, min_units));
             return (li.most + parts - 1) / parts * parts;
         }
         const int pad = (li.most + 11) / 12 * 12;
@@ -136,13 +141,12 @@ struct Line {
                    ? pad
                    : 0;
     }
-    // Units of one CTA's run: an equal share, but not so small that a tile's join
-    // costs more than its keys, unless whole tiles are smaller.  Of tiles counted
-    // alike, a CTA takes an equal part of one, or with more tiles than CTAs a
+    // Units of one CTA's run: an equal share, but least_units at least.  Of tiles
+    // counted alike, a CTA takes an equal part of one, or with more tiles than CTAs a
     // multiple of a whole, a half, a third or a quarter: the first of these that
     // gives away at most 1/16 of the share, else the one that gives away least.
     __host__ __device__ static int run_units(const LineInfo &li, int items, int n_ctas, int min_units) {
-        const int least = min(li.most, min_units);
+        const int least = least_units(li, min_units);
         if (li.pad && items * 4 < n_ctas * 3) return li.pad / min(n_ctas / items, li.most / least);
         const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
         if (!li.pad) return max(share, least);

@@ -48,7 +48,9 @@ constexpr int HK = TK / 2;                  // keys of half a tile
 constexpr int TR = 128;                     // query rows of a tile
 constexpr int kPagesPerTile = TK / kBlockTokens;
 constexpr uint32_t kWaitNs = 1000000000u;   // 1 s
-constexpr int kMinTiles = 8;                // of a CTA's run: below, a join costs more than the keys
+// Key tiles of a CTA's run.  With 8, nine ragged sequences of up to 1501 keys took
+// 47.0 us (37.0 with 4) and 32 query tokens over 4096 keys 30.5 (23.7).
+constexpr int kMinTiles = 4;
 constexpr float kMoveMax = 8.f;             // log2 units a tile may exceed m by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
@@ -176,77 +178,92 @@ __device__ __forceinline__ uint32_t f16_of_bf16(uint32_t two, float f) {
     return pack_f16(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xFFFF0000u) * f);
 }
 
-// U row quads (x, x + 256, ...) of a shared tile's rows [r0, r0 + nr): the
-// parts' sums joined in CTA order against a running maximum, P parts' loads in
-// flight at a time (a load of what another SM has just written takes about 1000
-// cycles).
-template <int D, int RB, int U, int P>
-__device__ __forceinline__ void join_quads(const AttendArgs &a, const Seg &sh, int r0, int nr, int x) {
-    constexpr size_t REC = (size_t)RB * (D + 2);
-    const int n = sh.n_ctas, last = nr * (D / 4) - 1;
-    int row[U], q[U];
-    float m[U], l[U];
-    float4 o[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = min(x + u * 256, last);
-        q[u] = i / nr;
-        row[u] = r0 + i - q[u] * nr;
-        m[u] = -INFINITY;
-        l[u] = 0.f;
-        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll 1
-    for (int p0 = 0; p0 < n; p0 += P) {
-        float pm[P][U], pl[P][U];
-        float4 v[P][U];
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int pp = min(p0 + p, n - 1);
-            const float *r = a.part + part_slot(sh.c0 + pp, pp == 0) * REC;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                pm[p][u] = __ldcg(r + (size_t)RB * D + row[u]);
-                pl[p][u] = __ldcg(r + (size_t)RB * (D + 1) + row[u]);
-                v[p][u] = __ldcg(reinterpret_cast<const float4 *>(r) + (size_t)q[u] * RB + row[u]);
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (p0 + p >= n) continue;
-                const float mm = fmaxf(m[u], pm[p][u]), base = mm == -INFINITY ? 0.f : mm;
-                const float f = ex2(m[u] - base), w = ex2(pm[p][u] - base);
-                m[u] = mm;
-                l[u] = l[u] * f + pl[p][u] * w;
-                o[u].x = o[u].x * f + v[p][u].x * w;
-                o[u].y = o[u].y * f + v[p][u].y * w;
-                o[u].z = o[u].z * f + v[p][u].z * w;
-                o[u].w = o[u].w * f + v[p][u].w * w;
-            }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (x + u * 256 > last) continue;
-        const float inv = l[u] > 0.f ? 1.f / l[u] : (l[u] == 0.f ? 0.f : l[u]);
-        const int qrow = sh.rbase + row[u], tok = token_of(qrow, a.gqa_inv), h = sh.g * a.gqa + qrow - tok * a.gqa;
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                   (int64_t)(sh.q0 + tok) * a.out_stride + (int64_t)h * D + q[u] * 4) =
-            make_uint2(pack_bf16(o[u].x * inv, o[u].y * inv), pack_bf16(o[u].z * inv, o[u].w * inv));
-        if (q[u] == 0 && a.lse)
-            a.lse[(int64_t)(sh.q0 + tok) * a.H + h] =
-                m[u] == -INFINITY ? -INFINITY : m[u] * kLn2 + logf(l[u]);
-    }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// This CTA's share (the part-th of n_ctas) of a shared tile's rows, by 256 threads.
-template <int D, int RB>
-__device__ __forceinline__ void join_rows(const AttendArgs &a, const Seg &sh, int part, int t) {
+// This CTA's share (the part-th of n_ctas) of a shared tile's rows, by 256 threads
+// (t) that meet(): the parts' sums joined in CTA order.  The parts come through
+// shared memory (`buf`, `bytes` of it; ml: 2 floats for each part of each row), all
+// of them in flight at once, by loops that are short because they run once, out of
+// a cold instruction cache: loaded into registers eight at a time, the joins of nine
+// ragged sequences took 10 to 22 thousand cycles.
+template <int D, int RB, class Meet>
+__device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, int part, int t, uint8_t *buf,
+                                          int bytes, float *ml, Meet meet) {
+    constexpr int QUADS = D / 4;
+    constexpr size_t REC = (size_t)RB * (D + 2);
     const int rows = min(RB, sh.q_len * a.gqa - sh.rbase), n = sh.n_ctas;
     const int r0 = rows * part / n, nr = rows * (part + 1) / n - r0;
+    if (nr == 0) return true;
+    auto record = [&](int p) { return a.part + part_slot(sh.c0 + p, p == 0) * REC; };
+    float *weight = ml, *sums = ml + n * nr;             // [part][row]; sums[row]: then 1 / l
+    // x / y by y_inv = ceil(2^32 / y), where x * y < 2^32 (an x is below 32 (RB + n),
+    // a y at most RB); 2^32 is 0 for y = 1
+    auto div = [](int x, uint32_t y_inv) { return y_inv ? (int)__umulhi((uint32_t)x, y_inv) : x; };
+    const uint32_t nr_inv = ~0u / (uint32_t)nr + 1;
+    const int most = min(QUADS, bytes / (n * nr * 16));  // quads of a row at a time
 #pragma unroll 1
-    for (int x = t; x < nr * (D / 4); x += 256 * 2) join_quads<D, RB, 2, 4>(a, sh, r0, nr, x);
+    for (int q0 = 0; q0 < QUADS; q0 += most) {
+        const int nq = min(most, QUADS - q0);
+#pragma unroll 1
+        for (int x = t; x < n * nq * nr; x += 256) {     // [part][quad][row]
+            const int y = div(x, nr_inv), p = div(y, ~0u / (uint32_t)nq + 1);
+            copy16(tc::smem_u32(buf) + x * 16, reinterpret_cast<const float4 *>(record(p)) +
+                                                   (size_t)(q0 + y - p * nq) * RB + r0 + x - y * nr);
+        }
+        if (q0 == 0) {
+#pragma unroll 1
+            for (int x = t; x < n * nr; x += 256) {
+                const int p = div(x, nr_inv), r = r0 + x - p * nr;
+                weight[x] = __ldcg(record(p) + (size_t)RB * D + r);
+                sums[x] = __ldcg(record(p) + (size_t)RB * (D + 1) + r);
+            }
+            if (!meet()) return false;
+            if (t < nr) {
+                float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+                for (int p = 0; p < n; ++p) m = fmaxf(m, weight[p * nr + t]);
+                const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+                for (int p = 0; p < n; ++p) {
+                    const float w = ex2(weight[p * nr + t] - base);
+                    weight[p * nr + t] = w;
+                    l += w * sums[p * nr + t];
+                }
+                sums[t] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+                const int qrow = sh.rbase + r0 + t, tok = token_of(qrow, a.gqa_inv);
+                if (a.lse)
+                    a.lse[(int64_t)(sh.q0 + tok) * a.H + sh.g * a.gqa + qrow - tok * a.gqa] =
+                        m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (!meet()) return false;
+#pragma unroll 1
+        for (int x = t; x < nr * nq; x += 256) {
+            const int q = div(x, nr_inv), r = x - q * nr;
+            const float4 *v = reinterpret_cast<const float4 *>(buf) + x;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int p = 0; p < n; ++p) {
+                const float w = weight[p * nr + r];
+                const float4 y = v[p * nq * nr];
+                o.x += w * y.x;
+                o.y += w * y.y;
+                o.z += w * y.z;
+                o.w += w * y.w;
+            }
+            const float inv = sums[r];
+            const int qrow = sh.rbase + r0 + r, tok = token_of(qrow, a.gqa_inv);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                       (int64_t)(sh.q0 + tok) * a.out_stride +
+                                       (int64_t)(sh.g * a.gqa + qrow - tok * a.gqa) * D + (q0 + q) * 4) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        }
+        if (!meet()) return false;                       // shared memory is free
+    }
+    return true;
 }
 
 }  // namespace
@@ -942,8 +959,11 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
             if (!meet(1, met1++ & 1)) break;
             const bool all = bar->go != 0;
-            if (all) join_rows<D, RB>(a, sh, blockIdx.x - sh.c0, tid - 128);
-            if (!meet(1, met1++ & 1)) break;             // go and the counters are free
+            auto met_all = [&] { return meet(1, met1++ & 1); };
+            if (all && !join_rows<D, RB>(a, sh, blockIdx.x - sh.c0, tid - 128, kvs, NS * LY::TILE,
+                                         reinterpret_cast<float *>(qs), met_all))
+                break;
+            if (!met_all()) break;                       // go and the counters are free
             if (tid == 128) {
                 // the last CTA to leave readies the counters for the next call
                 __threadfence();
