@@ -184,7 +184,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
 
 // This CTA's share (the part-th of n_ctas) of a shared tile's rows, by 256 threads
 // (t) that meet(): the parts' sums joined in CTA order.  The parts come through
-// shared memory (`buf`, `bytes` of it; ml: 2 floats for each part of each row), all
+// shared memory (`buf`, `bytes` of it; ml: 4 floats for each part of each row), all
 // of them in flight at once, by loops that are short because they run once, out of
 // a cold instruction cache: loaded into registers eight at a time, the joins of nine
 // ragged sequences took 10 to 22 thousand cycles.
@@ -197,7 +197,8 @@ __device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, in
     const int r0 = rows * part / n, nr = rows * (part + 1) / n - r0;
     if (nr == 0) return true;
     auto record = [&](int p) { return a.part + part_slot(sh.c0 + p, p == 0) * REC; };
-    float *weight = ml, *sums = ml + n * nr;             // [part][row]; sums[row]: then 1 / l
+    // [part][row]: m and l; then the part's weight w, and w l
+    float2 *ml_of = reinterpret_cast<float2 *>(ml), *w_of = ml_of + n * nr;
     // x / y by y_inv = ceil(2^32 / y), where x * y < 2^32 (an x is below 32 (RB + n),
     // a y at most RB); 2^32 is 0 for y = 1
     auto div = [](int x, uint32_t y_inv) { return y_inv ? (int)__umulhi((uint32_t)x, y_inv) : x; };
@@ -206,7 +207,7 @@ __device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, in
 #pragma unroll 1
     for (int q0 = 0; q0 < QUADS; q0 += most) {
         const int nq = min(most, QUADS - q0);
-#pragma unroll 1
+#pragma unroll 4
         for (int x = t; x < n * nq * nr; x += 256) {     // [part][quad][row]
             const int y = div(x, nr_inv), p = div(y, ~0u / (uint32_t)nq + 1);
             copy16(tc::smem_u32(buf) + x * 16, reinterpret_cast<const float4 *>(record(p)) +
@@ -216,26 +217,18 @@ __device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, in
 #pragma unroll 1
             for (int x = t; x < n * nr; x += 256) {
                 const int p = div(x, nr_inv), r = r0 + x - p * nr;
-                weight[x] = __ldcg(record(p) + (size_t)RB * D + r);
-                sums[x] = __ldcg(record(p) + (size_t)RB * (D + 1) + r);
+                const float *rec = record(p) + (size_t)RB * D + r;
+                ml_of[x] = make_float2(__ldcg(rec), __ldcg(rec + RB));
             }
             if (!meet()) return false;
-            if (t < nr) {
-                float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+            for (int x = t; x < n * nr; x += 256) {
+                const int r = x - div(x, nr_inv) * nr;
+                float m = -INFINITY;
 #pragma unroll 4
-                for (int p = 0; p < n; ++p) m = fmaxf(m, weight[p * nr + t]);
-                const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-                for (int p = 0; p < n; ++p) {
-                    const float w = ex2(weight[p * nr + t] - base);
-                    weight[p * nr + t] = w;
-                    l += w * sums[p * nr + t];
-                }
-                sums[t] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-                const int qrow = sh.rbase + r0 + t, tok = token_of(qrow, a.gqa_inv);
-                if (a.lse)
-                    a.lse[(int64_t)(sh.q0 + tok) * a.H + sh.g * a.gqa + qrow - tok * a.gqa] =
-                        m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+                for (int p = 0; p < n; ++p) m = fmaxf(m, ml_of[p * nr + r].x);
+                const float w = ex2(ml_of[x].x - (m == -INFINITY ? 0.f : m));
+                w_of[x] = make_float2(w, w * ml_of[x].y);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -245,21 +238,29 @@ __device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, in
             const int q = div(x, nr_inv), r = x - q * nr;
             const float4 *v = reinterpret_cast<const float4 *>(buf) + x;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
 #pragma unroll 4
             for (int p = 0; p < n; ++p) {
-                const float w = weight[p * nr + r];
+                const float2 w = w_of[p * nr + r];
                 const float4 y = v[p * nq * nr];
-                o.x += w * y.x;
-                o.y += w * y.y;
-                o.z += w * y.z;
-                o.w += w * y.w;
+                l += w.y;
+                o.x += w.x * y.x;
+                o.y += w.x * y.y;
+                o.z += w.x * y.z;
+                o.w += w.x * y.w;
             }
-            const float inv = sums[r];
+            const float inv = l > 0.f ? __fdividef(1.f, l) : (l == 0.f ? 0.f : l);   // l < 2^32
             const int qrow = sh.rbase + r0 + r, tok = token_of(qrow, a.gqa_inv);
+            const int h = sh.g * a.gqa + qrow - tok * a.gqa;
             *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                       (int64_t)(sh.q0 + tok) * a.out_stride +
-                                       (int64_t)(sh.g * a.gqa + qrow - tok * a.gqa) * D + (q0 + q) * 4) =
+                                       (int64_t)(sh.q0 + tok) * a.out_stride + (int64_t)h * D + (q0 + q) * 4) =
                 make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+            if (q0 + q == 0 && a.lse) {
+                float m = -INFINITY;
+#pragma unroll 1
+                for (int p = 0; p < n; ++p) m = fmaxf(m, ml_of[p * nr + r].x);
+                a.lse[(int64_t)(sh.q0 + tok) * a.H + h] = m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
+            }
         }
         if (!meet()) return false;                       // shared memory is free
     }
