@@ -160,6 +160,13 @@ __device__ __forceinline__ uint32_t e4m3_f16(uint32_t two) {
     return r;
 }
 
+// 16 bytes to shared memory, zeros when `there` is false (nothing is read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there = true) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
 // The largest biased exponent of 8 bf16, and the power of two that a query row
 // with that largest exponent is divided by on its way to f16 (kept where it and
 // its inverse are normal float32; none for a row of zeros).
@@ -176,10 +183,6 @@ __device__ __forceinline__ int row_exponent(int biased) {
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ uint32_t f16_of_bf16(uint32_t two, float f) {
     return pack_f16(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xFFFF0000u) * f);
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // This CTA's share (the part-th of n_ctas) of a shared tile's rows, by 256 threads
@@ -624,43 +627,58 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
                                                (int64_t)seg->q0 * a.q_stride +
                                                (int64_t)seg->g * a.gqa * D;
-                    // four loads in flight at a time, in a loop: unrolled whole, fetching its
-                    // instructions took three times as long as the loads
+                    // all of a thread's chunks in flight at once, asked for by a short loop
+                    // (four at a time through registers, they took 7 thousand cycles)
                     constexpr int CPR = D / 8, RPP = 128 / CPR;       // chunks of a row, rows of a pass
                     constexpr int N = (PAIR ? TR : TR / 2) / RPP;     // a thread's chunks
                     const int c16 = (tid & 127) % CPR, rr = r0 + (tid & 127) / CPR;
                     src += c16 * 8;
                     dst += (c16 >> 3) * LY::ATOM;
+                    auto chunk = [&](int i) {
+                        const int r = rr + i * RPP;
+                        return reinterpret_cast<uint4 *>(dst + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+                    };
 #pragma unroll 1
-                    for (int i0 = 0; i0 < N; i0 += 4) {
-                        uint4 v[4];
+                    for (int i = 0; i < N; ++i) {
+                        const int qrow = base + rr + i * RPP, t = token_of(qrow, a.gqa_inv);
+                        copy16(tc::smem_u32(chunk(i)), src + (int64_t)t * a.q_stride + (qrow - t * a.gqa) * D,
+                               qrow < rows_all);
+                    }
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    if (E4 || flip || !keep) {
+                        // each thread's own chunks: the scale's sign; E4: to f16, the row's
+                        // largest entry in [1, 2)
+                        constexpr int B = 4;
+#pragma unroll 1
+                        for (int i0 = 0; i0 < N; i0 += B) {
+                            uint4 x[B];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int qrow = base + rr + (i0 + i) * RPP;
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if (qrow < rows_all) {
-                                const int t = token_of(qrow, a.gqa_inv), h = qrow - t * a.gqa;
-                                v[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                    src + (int64_t)t * a.q_stride + h * D));
+                            for (int i = 0; i < B; ++i) {
+                                x[i] = *chunk(i0 + i);
+                                x[i] = make_uint4((x[i].x ^ flip) & keep, (x[i].y ^ flip) & keep,
+                                                  (x[i].z ^ flip) & keep, (x[i].w ^ flip) & keep);
                             }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = rr + (i0 + i) * RPP;
-                            uint4 x = make_uint4((v[i].x ^ flip) & keep, (v[i].y ^ flip) & keep,
-                                                 (v[i].z ^ flip) & keep, (v[i].w ^ flip) & keep);
                             if constexpr (E4) {
-                                // f16, the row's largest entry in [1, 2)
-                                int e = max_exponent(x);
+                                int e[B];
+#pragma unroll
+                                for (int i = 0; i < B; ++i) e[i] = max_exponent(x[i]);
 #pragma unroll
                                 for (int o = 1; o < CPR; o <<= 1)
-                                    e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-                                const float dn = pow2i(-row_exponent(e));
-                                x = make_uint4(f16_of_bf16(x.x, dn), f16_of_bf16(x.y, dn),
-                                               f16_of_bf16(x.z, dn), f16_of_bf16(x.w, dn));
-                                if (c16 == 0) qpow[(PAIR ? gr * TR : 0) + r] = pow2i(row_exponent(e));
+#pragma unroll
+                                    for (int i = 0; i < B; ++i)
+                                        e[i] = max(e[i], __shfl_xor_sync(0xffffffffu, e[i], o));
+#pragma unroll
+                                for (int i = 0; i < B; ++i) {
+                                    const float dn = pow2i(-row_exponent(e[i]));
+                                    x[i] = make_uint4(f16_of_bf16(x[i].x, dn), f16_of_bf16(x[i].y, dn),
+                                                      f16_of_bf16(x[i].z, dn), f16_of_bf16(x[i].w, dn));
+                                    if (c16 == 0)
+                                        qpow[(PAIR ? gr * TR : 0) + rr + (i0 + i) * RPP] =
+                                            pow2i(row_exponent(e[i]));
+                                }
                             }
-                            *reinterpret_cast<uint4 *>(dst + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = x;
+#pragma unroll
+                            for (int i = 0; i < B; ++i) *chunk(i0 + i) = x[i];
                         }
                     }
                     tc::fence_proxy_async_smem();
@@ -879,7 +897,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (live && a.lse)
                         a.lse[(int64_t)(seg->q0 + tok) * a.H + h] =
                             m == -INFINITY ? -INFINITY : m * kLn2 + logf(l);
-                } else {
+                } else if (live) {
                     rec[(size_t)RB * D + prow] = m;
                     rec[(size_t)RB * (D + 1) + prow] = l;
                 }
@@ -919,7 +937,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                                     VecTraits<__nv_bfloat16>::pack(v);
                             }
                         }
-                    } else {
+                    } else if (live) {
                         // four columns of a row, rows adjacent
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
