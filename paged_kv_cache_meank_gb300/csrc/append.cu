@@ -1,22 +1,25 @@
 // New keys and values into a paged cache, K rotated on the way.
 //
-// A warp owns one (sequence, block, kv head) of either K or V: the up to 32 new
-// rows that fall into that block.  It reads them once into registers, a 16-byte
-// vector of the first half of a row and its rotate-half partners per lane.  For
-// scaled e4m3 pages the largest finite entry sets the block's power-of-two
-// scale; no other warp touches the block and head, so the scale, the codes
-// already there and the new rows change without atomics.  The scale bounds
-// |k| * sqrt(2), the largest entry that any rotation can make, so it holds at
-// every position the block is rotated to later (KVMem, "Virtualizing
-// Million-Token Agent Workspaces on a Consumer GPU", §4.4: raw K re-rotated at
-// compact positions), and raw K shares it.
+// A CTA owns one (sequence, block, kv head): the up to 32 new rows that fall into
+// that block, K by four warps and V by the other four.  They read the rows once
+// into registers, a 16-byte vector of the first half of a row and its rotate-half
+// partners per lane, at most four such pairs (with a warp to a block's K or V the
+// rows took 112 to 182 registers, and 8192 tokens of e4m3 pages with raw K 19.2 us
+// against 15.9; their 59 MB cannot take less than 8.6).  For scaled e4m3 pages
+// the largest finite entry sets the block's power-of-two scale; no other CTA
+// touches the block and head, so the scale, the codes already there and the new
+// rows change without atomics.  The scale bounds |k| * sqrt(2), the largest entry
+// that any rotation can make, so it holds at every position the block is rotated
+// to later (KVMem, "Virtualizing Million-Token Agent Workspaces on a Consumer
+// GPU", §4.4: raw K re-rotated at compact positions), and raw K shares it.
 // Memory bound: 2 G d elements read and 2 G d (3 with raw K) written a token.
 #include "kvm_internal.cuh"
 #include "kvm_vec.cuh"
 
 namespace kvm {
 
-constexpr int kAppendWarps = 8;
+constexpr int kParts = 4;                  // warps of a block's K or V, 32 / kParts rows each
+constexpr int kAppendThreads = 2 * kParts * 32;
 // The largest raw entry a block of scale 1 takes (e4m3: 448 / sqrt(2) rounded
 // down for K, 448 for V), as mantissa in [1, 2) times 2^8.
 constexpr float kMostK = 316.75f, kMostV = 448.0f;
@@ -32,50 +35,43 @@ __device__ inline int scale_exponent(float amax, float most) {
 __device__ inline float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 template <typename T, typename TP, int D, bool SCALED>
-__global__ void __launch_bounds__(kAppendWarps * 32)
-append_kernel(AppendArgs a, int spans, int units) {
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(AppendArgs a, int spans) {
     using VI = VecTraits<T>;
     using VP = VecTraits<TP>;
     // a lane's piece of a half row, in elements: the input's vector (8 bf16, or
     // 4 float32; a page vector of 8 e4m3 takes two float32 pieces' place)
     constexpr int N = VI::N, HD = D / 2, TPT = HD / N, RPW = 32 / TPT;
-    constexpr int ITERS = kBlockTokens / RPW;
+    constexpr int ITERS = kBlockTokens / kParts / RPW;
     using V = typename VI::V;
     const int lane = threadIdx.x & 31, c = lane % TPT, sub = lane / TPT;
     const int seq = blockIdx.x / spans, span = blockIdx.x - seq * spans;
-    const int unit = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
-    if (unit >= units) return;
-    const bool is_k = unit < a.b.G;
-    const int g = is_k ? unit : unit - a.b.G;
+    const int g = blockIdx.y, warp = threadIdx.x >> 5, part = warp % kParts;
+    const bool is_k = warp < kParts;
+    __shared__ float top[2 * kParts];                   // largest entry of each warp
 
     const int q0 = a.b.q_start[seq], q1 = a.b.q_start[seq + 1], kv = a.b.kv_len[seq];
     const int q_len = q1 - q0;
     if (q0 < 0 || q1 < q0 || q1 > a.b.n_tokens || q_len > a.b.max_q_len || kv < q_len ||
         kv > a.b.max_kv_len) {
-        if (lane == 0) atomicOr(a.b.err, kErrBatch);
+        if (threadIdx.x == 0) atomicOr(a.b.err, kErrBatch);
         return;
     }
     const int first = kv - q_len;                       // logical index of token 0
     const int blk = first / kBlockTokens + span;
     const int lo = max(first, blk * kBlockTokens), hi = min(kv, (blk + 1) * kBlockTokens);
     if (lo >= hi) return;
-    const int64_t at = (int64_t)seq * a.b.table_stride + blk;
-    const int64_t page = a.b.page_table[at];
-    const int64_t srow = SCALED && a.b.scale_rows ? (int64_t)a.b.scale_rows[at] : page;
-    if (page < 0 || page >= a.b.n_pages || (SCALED && (srow < 0 || srow >= a.b.n_scale_rows))) {
-        if (lane == 0) atomicOr(a.b.err, kErrBatch);
-        return;
-    }
     const int r0 = lo - blk * kBlockTokens, n = hi - lo;   // rows [r0, r0 + n) of the page
     const int tok0 = q0 + lo - first;
 
+    // the rows are asked for before their page is looked up: one wait, not two
     const T *src = is_k ? static_cast<const T *>(a.k) : static_cast<const T *>(a.v);
     const int64_t stride = is_k ? a.k_stride : a.v_stride;
     V vx[ITERS], vy[ITERS];
     uint32_t on = 0;                                    // bit i: this lane's row i is written
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-        const int j = i * RPW + sub;
+        const int j = (part * ITERS + i) * RPW + sub;
         if (j < n) {
             const int64_t pos = a.positions ? (int64_t)a.positions[tok0 + j] : (int64_t)(lo + j);
             if (pos < 0 || pos >= a.max_positions) {
@@ -88,13 +84,21 @@ append_kernel(AppendArgs a, int spans, int units) {
             ld_stream_v(p + HD, vy[i]);
         }
     }
-    if (!__any_sync(0xffffffffu, on != 0)) return;
+    const int64_t at = (int64_t)seq * a.b.table_stride + blk;
+    const int64_t page = a.b.page_table[at];
+    const int64_t srow = SCALED && a.b.scale_rows ? (int64_t)a.b.scale_rows[at] : page;
+    if (page < 0 || page >= a.b.n_pages || (SCALED && (srow < 0 || srow >= a.b.n_scale_rows))) {
+        if (threadIdx.x == 0) atomicOr(a.b.err, kErrBatch);
+        return;
+    }
     const size_t head = (((size_t)page * a.b.L + a.b.layer) * a.b.G + g) * kBlockTokens * D;
     TP *dst = (is_k ? static_cast<TP *>(a.k_pages) : static_cast<TP *>(a.v_pages)) + head;
     TP *raw = is_k && a.raw_pages ? static_cast<TP *>(a.raw_pages) + head : nullptr;
 
     float inv = 1.f;
     if constexpr (SCALED) {
+        float *sp = (is_k ? a.k_scale : a.v_scale) + ((size_t)srow * a.b.L + a.b.layer) * a.b.G + g;
+        const float old = r0 > 0 ? *sp : 0.f;           // read by all before one writes
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
@@ -112,17 +116,20 @@ append_kernel(AppendArgs a, int spans, int units) {
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float *sp = (is_k ? a.k_scale : a.v_scale) + ((size_t)srow * a.b.L + a.b.layer) * a.b.G + g;
+        if (lane == 0) top[warp] = amax;
+        if (!__syncthreads_or(on != 0)) return;         // (K's and V's positions are the same)
+#pragma unroll
+        for (int w = 0; w < kParts; ++w) amax = fmaxf(amax, top[warp - part + w]);
         float scale = pow2f(scale_exponent(amax, is_k ? kMostK : kMostV));
         if (r0 > 0) {
-            const float old = checked_scale(*sp, a.b.err);
-            if (old >= scale) {
-                scale = old;
+            const float had = checked_scale(old, a.b.err);
+            if (had >= scale) {
+                scale = had;
             } else {
                 // the codes of the rows before follow the larger scale
-                const float f = old / scale;
+                const float f = had / scale;
                 const int vecs = r0 * (D / VP::N);
-                for (int i = lane; i < vecs; i += 32) {
+                for (int i = part * 32 + lane; i < vecs; i += kParts * 32) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         TP *p = w == 0 ? dst : raw;
@@ -137,14 +144,13 @@ append_kernel(AppendArgs a, int spans, int units) {
                 }
             }
         }
-        __syncwarp();                                   // every lane has read the old scale
-        if (lane == 0) *sp = scale;
+        if (part == 0 && lane == 0) *sp = scale;
         inv = 1.f / scale;                              // exact: a power of two
     }
 
 #pragma unroll
     for (int i = 0; i < ITERS; ++i) {
-        const int j = i * RPW + sub;
+        const int j = (part * ITERS + i) * RPW + sub;
         if (!(on >> i & 1)) continue;
         float x[N], y[N], ox[N], oy[N];
         VI::unpack(vx[i], x);
@@ -152,12 +158,14 @@ append_kernel(AppendArgs a, int spans, int units) {
         TP *row = dst + (size_t)(r0 + j) * D + c * N;
         if (is_k) {
             const int64_t pos = a.positions ? (int64_t)a.positions[tok0 + j] : (int64_t)(lo + j);
-            const float2 *t = a.table + pos * HD + c * N;
+            const float4 *t = reinterpret_cast<const float4 *>(a.table + pos * HD + c * N);
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const float2 w = __ldg(t + k);
+            for (int k = 0; k < N; k += 2) {
+                const float4 w = __ldg(t + k / 2);
                 ox[k] = __fsub_rn(__fmul_rn(x[k], w.x), __fmul_rn(y[k], w.y)) * inv;
                 oy[k] = __fadd_rn(__fmul_rn(x[k], w.y), __fmul_rn(y[k], w.x)) * inv;
+                ox[k + 1] = __fsub_rn(__fmul_rn(x[k + 1], w.z), __fmul_rn(y[k + 1], w.w)) * inv;
+                oy[k + 1] = __fadd_rn(__fmul_rn(x[k + 1], w.w), __fmul_rn(y[k + 1], w.z)) * inv;
             }
             if (raw != nullptr) {
 #pragma unroll
@@ -185,12 +193,10 @@ template <typename T, typename TP, int D, bool SCALED>
 static cudaError_t append_t(const AppendArgs &a, cudaStream_t s) {
     // a run of max_q_len tokens touches at most this many blocks
     const int spans = (a.b.max_q_len + 2 * kBlockTokens - 2) / kBlockTokens;
-    const int units = 2 * a.b.G;
     const int64_t gx = (int64_t)a.b.n_seqs * spans;
-    const int gy = (units + kAppendWarps - 1) / kAppendWarps;
-    if (gx > 0x7FFFFFFF || gy > 65535) return cudaErrorInvalidValue;
+    if (gx > 0x7FFFFFFF || a.b.G > 65535) return cudaErrorInvalidValue;
     append_kernel<T, TP, D, SCALED>
-        <<<dim3((unsigned)gx, (unsigned)gy), kAppendWarps * 32, 0, s>>>(a, spans, units);
+        <<<dim3((unsigned)gx, (unsigned)a.b.G), kAppendThreads, 0, s>>>(a, spans);
     note_launch();
     return cudaGetLastError();
 }

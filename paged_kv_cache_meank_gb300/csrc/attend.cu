@@ -106,28 +106,39 @@ attend_simt_kernel(AttendArgs a, int min_units) {
                 using V = typename VecTraits<T>::V;
                 const size_t base = (((size_t)page * a.b.L + a.b.layer) * a.b.G + k.g) *
                                     kBlockTokens * D;
-                const int first = KS ? lane : tid, step = KS ? 32 : kWarps * 32;
-                for (int i = first; i < 2 * kBlockTokens * VPR; i += step) {
-                    const bool is_v = i >= kBlockTokens * VPR;
-                    const int j = is_v ? i - kBlockTokens * VPR : i;
-                    const int row = j / VPR, c = (j - row * VPR) * N;
-                    float f[N];
-                    if (ok && key0 + row < k.i.kv) {
-                        V v;
-                        ld_stream_v(typed<T>(is_v ? a.v_pages : a.k_pages) + base + row * D + c, v);
-                        VecTraits<T>::unpack(v, f);
-                        const float sc = is_v ? vs : ks;
+                // eight loads in flight a thread: a page's latency is met four to eight
+                // times, not once for each of its 4 KB
+                constexpr int TOTAL = 2 * kBlockTokens * VPR, STEP = KS ? 32 : kWarps * 32;
+                constexpr int U = TOTAL / STEP < 8 ? TOTAL / STEP : 8;
+#pragma unroll 1
+                for (int i0 = KS ? lane : tid; i0 < TOTAL; i0 += U * STEP) {
+                    V v[U];
 #pragma unroll
-                        for (int e = 0; e < N; ++e) f[e] *= sc;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < N; ++e) f[e] = 0.f;
+                    for (int x = 0; x < U; ++x) {
+                        const int i = i0 + x * STEP, j = i % (kBlockTokens * VPR);
+                        if (ok && key0 + j / VPR < k.i.kv)
+                            ld_stream_v(typed<T>(i == j ? a.k_pages : a.v_pages) + base + (size_t)j * N, v[x]);
                     }
-                    float *dst = is_v ? vb + row * D + c : kb + row * LY::KST + c;
 #pragma unroll
-                    for (int e = 0; e < N; e += 4)
-                        *reinterpret_cast<float4 *>(dst + e) =
-                            make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                    for (int x = 0; x < U; ++x) {
+                        const int i = i0 + x * STEP, j = i % (kBlockTokens * VPR);
+                        const int row = j / VPR, c = (j - row * VPR) * N;
+                        float f[N];
+                        if (ok && key0 + row < k.i.kv) {
+                            VecTraits<T>::unpack(v[x], f);
+                            const float sc = i == j ? ks : vs;
+#pragma unroll
+                            for (int e = 0; e < N; ++e) f[e] *= sc;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < N; ++e) f[e] = 0.f;
+                        }
+                        float *dst = i == j ? kb + row * LY::KST + c : vb + row * D + c;
+#pragma unroll
+                        for (int e = 0; e < N; e += 4)
+                            *reinterpret_cast<float4 *>(dst + e) =
+                                make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                    }
                 }
             }
             if (KS) __syncwarp(); else __syncthreads();
