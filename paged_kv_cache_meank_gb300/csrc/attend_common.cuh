@@ -118,61 +118,56 @@ struct Line {
         return li;
     }
     // From the row tiles' number, their units and the longest one's: what they are
-    // counted as, and the runs.
+    // counted as, and the runs.  A join counts as `join` units.
     template <bool PAD>
     __host__ __device__ static void plan(LineInfo &li, int items, int n_ctas, int min_units) {
         const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
+        // below min_units a tile's join costs more than its keys, and a tile of twice
+        // that is not cut
+        const int join = 2 * min_units, least = li.most <= join ? li.most : min_units;
+        li.per = max(share, least);
+        if (!PAD || items == 0) return;
         // A CTA to a tile, and no joins, where the longest takes less longer than an
-        // equal share than a join does (counted as twice min_units): nine ragged
-        // sequences of up to 1501 keys took 36.8 us with runs of equal shares, 26.4 so.
-        if (PAD && items <= n_ctas && li.most <= share + 2 * min_units) {
+        // equal share than a join does: nine ragged sequences of up to 1501 keys took
+        // 36.8 us with runs of equal shares, 26.4 so.
+        if (items <= n_ctas && li.most <= share + join) {
             li.pad = li.per = li.most;
             li.total = items * li.most;
             return;
         }
-        if (PAD) li.pad = padded_weight(items, li, n_ctas, min_units);
-        if (li.pad) li.total = items * li.pad;
-        li.per = run_units(li, items, n_ctas, min_units);
-    }
-    // The shortest run: below min_units a tile's join costs more than its keys, and a
-    // tile of twice that is not cut.
-    __host__ __device__ static int least_units(const LineInfo &li, int min_units) {
-        return li.most <= 2 * min_units ? li.most : min_units;
-    }
-    // Where the row tiles are about equally long, they are all counted as `pad`
-    // units, at least the longest one's: runs then begin and end at the same few
-    // places of every tile (run_units).  A CTA meets one tile and not the ends of
-    // two, and CTAs that share a head's keys read them at the same time (begun at
-    // scattered keys they read 762 MB of a 134 MB cache).
-    __host__ __device__ static int padded_weight(int items, const LineInfo &li, int n_ctas, int min_units) {
-        if (items == 0 || (float)li.total < 0.85f * (float)items * (float)li.most) return 0;
-        if (items * 4 < n_ctas * 3) {                    // several CTAs to a tile
-            const int parts = min(n_ctas / items, li.most / least_units(li, min_units));
-            return (li.most + parts - 1) / parts * parts;
+        // Where the row tiles are about equally long, they are all counted as `pad`
+        // units, at least the longest one's: runs then begin and end at the same few
+        // places of every tile.  A CTA meets one tile and not the ends of two, and
+        // CTAs that share a head's keys read them at the same time (begun at scattered
+        // keys they read 762 MB of a 134 MB cache).
+        if ((float)li.total < 0.85f * (float)items * (float)li.most) return;
+        int most_per = 0x7FFFFFFF;                       // what another split has to beat
+        if (items < n_ctas) {                            // an equal part of a tile to a CTA
+            const int parts = min(n_ctas / items, li.most / least);
+            li.per = (li.most + parts - 1) / parts;
+            li.pad = li.per * parts;
+            most_per = (li.per + (parts > 1 ? join : 0)) / 8 * 7 - join;
         }
+        // A multiple of a whole tile, its half, third, fourth or sixth: the first of
+        // these that gives away at most 1/16 of the share, else the one that gives away
+        // least; not where few CTAs are idle with an equal part (512 query tokens over
+        // 16384 keys are 96 tiles, and took 210 us by 96 CTAs, 168 by all).
         const int pad = (li.most + 11) / 12 * 12;
-        return li.most >= 24 && (float)li.total >= 0.85f * (float)items * (float)pad &&
-                       (float)items * (float)pad < 2147483647.f
-                   ? pad
-                   : 0;
-    }
-    // Units of one CTA's run: an equal share, but least_units at least.  Of tiles
-    // counted alike, a CTA takes an equal part of one, or with more tiles than CTAs a
-    // multiple of a whole, a half, a third or a quarter: the first of these that
-    // gives away at most 1/16 of the share, else the one that gives away least.
-    __host__ __device__ static int run_units(const LineInfo &li, int items, int n_ctas, int min_units) {
-        const int least = least_units(li, min_units);
-        if (li.pad && items * 4 < n_ctas * 3) return li.pad / min(n_ctas / items, li.most / least);
-        const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
-        if (!li.pad) return max(share, least);
-        int best = 0;
+        const int per = (int)(((uint32_t)(items * pad) + n_ctas - 1) / (uint32_t)n_ctas);
+        if (li.most >= 24 && per < most_per && (float)li.total >= 0.85f * (float)items * (float)pad &&
+            (float)items * (float)pad < 2147483647.f) {
+            int run = 0x7FFFFFFF;
 #pragma unroll 1
-        for (int m = 1; m <= 4; ++m) {
-            const int part = li.pad / m, run = (share + part - 1) / part * part;
-            if (best == 0 || run < best) best = run;
-            if (run - share <= share / 16) return run;
+            for (int m = 1; m <= 6 && run - per > per / 16; m += m < 4 ? 1 : 2) {
+                const int part = pad / m;
+                run = min(run, (per + part - 1) / part * part);
+            }
+            if (run < most_per) {
+                li.per = run;
+                li.pad = pad;
+            }
         }
-        return best;
+        if (li.pad) li.total = items * li.pad;
     }
 };
 
