@@ -526,7 +526,7 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
  * are not finite do not set the scale: infinities saturate, NaN stays.
  * Each page written belongs to one sequence of the batch; a sequence with
  * kv_len < q_len raises the device error flag and is skipped.
- * Errors: KVM_ERR_INVALID_ARG, KVM_ERR_CAPACITY.
+ * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences.
  */
 kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cache,
                          int32_t layer, const void *k, int64_t k_stride, const void *v,
@@ -549,13 +549,22 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * Bases and strides multiples of 16 bytes; all buffers device memory.
  * softmax_scale is usually 1 / sqrt(d); finite.
  * bf16 queries over bf16 or e4m3 pages run on the tensor cores: products and
- * sums in float32, with the weights rounded to 16 bits before the product
- * with V.  Every other pairing of types runs in float32 throughout.
+ * sums in float32, with the weights rounded to bf16 before the product with V;
+ * over e4m3 pages each weight times its v_scale is rounded to float16 against the
+ * largest such product of its row (below 2^-14 of it the rounding is absolute,
+ * 2^-25 of it at most).  Every other pairing of types runs in float32 throughout.
+ * Results do not depend on the order in which parts of the work end: the same
+ * call gives the same bits.
  * Cache rows at or behind kv_len are not read into the result whatever they
  * hold.  Rows below kv_len that causality hides from some queries of the batch
  * are read for the others and must hold finite values.
- * The call uses the context's workspace.
- * Errors: KVM_ERR_INVALID_ARG, KVM_ERR_CAPACITY.
+ * The call uses the context's workspace, captured calls too: calls of one
+ * context, eager or launched from graphs, follow one another on one stream or are
+ * ordered by events.
+ * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences or
+ * bounds whose work does not fit 32-bit counts (about 2^31 pieces of 32 keys for
+ * 4 query rows each, 2^32 / (H/G)^2 tokens).  kvm_sync reports KVM_ERR_TIMEOUT if
+ * one of the kernel's waits, all bounded to a second, gave up.
  */
 kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cache,
                       int32_t layer, const void *q, int64_t q_stride, float softmax_scale,

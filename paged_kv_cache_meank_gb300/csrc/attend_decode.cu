@@ -20,10 +20,14 @@
 // a power of two per row, the page's k_scale goes into the factor of the scores
 // and the weights times v_scale have a running maximum of their own.
 //
+// One sequence of 32768 bf16 keys takes 26.9 us, 19.0 of them its 134 MB at the
+// 7.06 TB/s that longer sequences add; the start (lengths, page numbers and keys,
+// each read before the next can be) takes 5 and leaving and joining the parts 3.  24
+// ragged sequences of e4m3 pages (508 MB) take 90.1 us, 5.6 TB/s.
 // Three 8 KB or four 4 KB stages a warp; eight to twelve warps an SM.  With fewer
 // tiles than SMs they are one CTA, for as few parts to join as can be: one
-// sequence of 32768 bf16 keys (134 MB) took 27.4 us against 31.4 with two CTAs of
-// four warps, of 65536 e4m3 keys 29.1 against 33.5.  With more, two or three CTAs,
+// sequence of 32768 bf16 keys took 27.4 us against 31.4 with two CTAs of four
+// warps, of 65536 e4m3 keys 29.1 against 33.5.  With more, two or three CTAs,
 // so that one streams while another joins; the third where rows are narrow and carry
 // more arithmetic for their bytes (24 ragged sequences of e4m3 pages: 94.6 us against
 // 101.3 with two).

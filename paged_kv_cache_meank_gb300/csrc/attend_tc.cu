@@ -25,10 +25,19 @@
 // factor of the page's scores; the weights times v_scale are kept in f16 against a
 // running maximum of their own, so scales of any size keep their precision.
 //
-// Warps: 0 TMA producer, 1 and 3 MMA issuers (one for each group), 2 walks the CTA's run of the work line
-// and hands its segments to the others, 4-7 and 8-11 softmax, e4m3:
-// 12-15 convert.  Registers move to the softmax warpgroups (setmaxnreg).  One CTA
-// per SM walks an equal run of the call's work line (attend_common.cuh).
+// Warps: 0 TMA producer, 1 and 3 MMA issuers (one for each group), 2 walks the
+// CTA's run of the work line and hands its segments to the others, 4-7 and 8-11
+// softmax, e4m3: 12-15 convert.  Registers move to the softmax warpgroups
+// (setmaxnreg).  One CTA per SM walks its run of the call's work line
+// (attend_common.cuh).
+// What bounds it: a pair of row tiles on one key tile takes 2 x (811 + 515) =
+// 2652 clocks of the tensor pipe as issued (the 64-key products read Q from shared
+// memory twice, 405 clocks a half where 256 would do; N = 128 would need the columns
+// that let a half be weighed while the other is made), and is passed in about
+// 2760: 2048 query tokens over 34816 bf16 keys (1.7 TFLOP) in 1.18 ms, 1440
+// TFLOP/s, 0.75 of the measured burst rate.  e4m3 pages add conversions and their
+// shared-memory traffic, about 4150 clocks: 32 tokens over 65568 keys 77 us.  Small
+// calls are bound by their start (9 thousand clocks to the first scores) and joins.
 // Every wait is bounded to a second; on timeout the device error flag (bit 4) is
 // raised and the CTA winds down as the scoring kernels do.
 #include <cuda.h>
