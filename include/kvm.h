@@ -526,7 +526,8 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
  * are not finite do not set the scale: infinities saturate, NaN stays.
  * Each page written belongs to one sequence of the batch; a sequence with
  * kv_len < q_len raises the device error flag and is skipped.
- * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences.
+ * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences or
+ * n_seqs * max_q_len beyond about 2^36.
  */
 kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cache,
                          int32_t layer, const void *k, int64_t k_stride, const void *v,
@@ -547,7 +548,7 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * out   device, q_dtype, token row i at out + i * out_stride elements.
  * lse   nullable, device float32 [n_tokens][H].
  * Bases and strides multiples of 16 bytes; all buffers device memory.
- * softmax_scale is usually 1 / sqrt(d); finite.
+ * softmax_scale is usually 1 / sqrt(d); at most 1e30 in magnitude.
  * bf16 queries over bf16 or e4m3 pages run on the tensor cores: products and
  * sums in float32, with the weights rounded to bf16 before the product with V;
  * over e4m3 pages each weight times its v_scale is rounded to float16 against the

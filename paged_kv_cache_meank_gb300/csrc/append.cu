@@ -191,12 +191,9 @@ append_kernel(AppendArgs a, int spans) {
 
 template <typename T, typename TP, int D, bool SCALED>
 static cudaError_t append_t(const AppendArgs &a, cudaStream_t s) {
-    // a run of max_q_len tokens touches at most this many blocks
-    const int spans = (a.b.max_q_len + 2 * kBlockTokens - 2) / kBlockTokens;
-    const int64_t gx = (int64_t)a.b.n_seqs * spans;
-    if (gx > 0x7FFFFFFF || a.b.G > 65535) return cudaErrorInvalidValue;
+    const int spans = append_spans(a.b.max_q_len);      // (the host has checked the grid's size)
     append_kernel<T, TP, D, SCALED>
-        <<<dim3((unsigned)gx, (unsigned)a.b.G), kAppendThreads, 0, s>>>(a, spans);
+        <<<dim3((unsigned)(a.b.n_seqs * spans), (unsigned)a.b.G), kAppendThreads, 0, s>>>(a, spans);
     note_launch();
     return cudaGetLastError();
 }

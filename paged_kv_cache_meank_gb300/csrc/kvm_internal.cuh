@@ -251,6 +251,8 @@ struct AppendArgs {
     const float2 *table;
     int64_t max_positions;
 };
+// Blocks that a run of max_q_len tokens touches at most.
+inline int append_spans(int max_q_len) { return (max_q_len + 2 * kBlockTokens - 2) / kBlockTokens; }
 cudaError_t launch_append(int q_dtype, int kv_dtype, int d, const AppendArgs &a, cudaStream_t s);
 
 struct AttendArgs {

@@ -220,6 +220,9 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
         return fail(KVM_ERR_INVALID_ARG, "K, V and raw K pages must differ");
     if (cache->k_scale && cache->k_scale == cache->v_scale)
         return fail(KVM_ERR_INVALID_ARG, "k_scale and v_scale must differ");
+    if ((int64_t)a.b.n_seqs * kvm::append_spans(a.b.max_q_len) > 0x7FFFFFFF || c.G > 65535)
+        return fail(KVM_ERR_CAPACITY, "batch: %d sequences of up to %d new tokens are too much for one call",
+                    batch->n_seqs, batch->max_q_len);
     KVM_TRY(row_stride(k_stride, c.G, c.d, c.q_dtype, "k"));
     KVM_TRY(row_stride(v_stride, c.G, c.d, c.q_dtype, "v"));
     KVM_TRY(on_device(k, c, "k"));
@@ -255,8 +258,9 @@ kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cac
     if (empty) return KVM_OK;
     if (!q || !out) return fail(KVM_ERR_INVALID_ARG, "q and out are required");
     if (causal != 0 && causal != 1) return fail(KVM_ERR_INVALID_ARG, "causal must be 0 or 1");
-    if (!std::isfinite(softmax_scale))
-        return fail(KVM_ERR_INVALID_ARG, "softmax_scale must be finite");
+    // (beyond that, the factor in log2 units could overflow)
+    if (!(std::fabs(softmax_scale) <= 1e30f))
+        return fail(KVM_ERR_INVALID_ARG, "softmax_scale must be at most 1e30 in magnitude");
     KVM_TRY(row_stride(q_stride, c.H, c.d, c.q_dtype, "q"));
     KVM_TRY(row_stride(out_stride, c.H, c.d, c.q_dtype, "out"));
     if (q == out) return fail(KVM_ERR_INVALID_ARG, "out must not be q");

@@ -267,6 +267,29 @@ def test_attend_refuses_batches_beyond_its_counts(kvm):
         check_attend(p, True, 64 ** -0.5, out, None)
 
 
+def test_append_refuses_batches_beyond_its_grid(kvm):
+    ctx = context(kvm, L=1, G=2, H=4, d=64, kv="bf16", act="bf16")
+    p = Paged([(1, 32)] * 1024, G=2, H=4, d=64, kv="bf16", act="bf16")
+    batch, cache = p.on(ctx)
+    q_start, kv_len, table, _ = batch.tensors
+    x = torch.zeros(p.n, 2, 64, device="cuda", dtype=torch.bfloat16)
+    big = ctx.batch(q_start, kv_len, table, n_tokens=p.n, max_q_len=2 ** 30 - 300, max_kv_len=32)
+    with pytest.raises(kvm.KvmError) as e:
+        ctx.append_kv(big, cache, 0, x, x)
+    assert e.value.name == "KVM_ERR_CAPACITY"
+
+
+def test_attend_refuses_scales_that_overflow(kvm):
+    ctx = context(kvm, L=1, G=2, H=4, d=64, kv="bf16", act="bf16")
+    p = Paged([(1, 32)], G=2, H=4, d=64, kv="bf16", act="bf16")
+    batch, cache = p.on(ctx)
+    out = torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16)
+    for scale in (2e30, -3e38, math.inf, math.nan):
+        with pytest.raises(kvm.KvmError) as e:
+            ctx.attend(batch, cache, 0, p.q.cuda(), out, scale=scale)
+        assert e.value.name == "KVM_ERR_INVALID_ARG"
+
+
 def test_a_call_with_nothing_to_do(kvm):
     """No sequences, no tokens, or sequences without tokens: nothing is written."""
     ctx = context(kvm, L=1, G=2, H=4, d=64, kv="bf16", act="bf16")
