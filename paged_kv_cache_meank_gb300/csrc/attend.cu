@@ -11,8 +11,8 @@
 // sums are joined at the end; otherwise the four warps take 4 rows each and
 // share the pages.
 // Bound by the CUDA cores' float32 rate and, for few keys, by latency: one token
-// over 77 float32 keys takes 8 us, most of it start-up (11.9 with a page's loads four
-// at a time).
+// over 77 float32 keys takes 5.9 us, most of it start-up (11.9 with a page's loads
+// four at a time).
 #include "attend_common.cuh"
 #include "kvm_vec.cuh"
 
@@ -109,10 +109,14 @@ attend_simt_kernel(AttendArgs a, int min_units) {
                 using V = typename VecTraits<T>::V;
                 const size_t base = (((size_t)page * a.b.L + a.b.layer) * a.b.G + k.g) *
                                     kBlockTokens * D;
-                // eight loads in flight a thread: a page's latency is met four to eight
-                // times, not once for each of its 4 KB
+                // Loads in flight a thread: eight, so that a page's latency is met a few
+                // times and not once for each of its 4 KB.  More where a warp reads
+                // float32 pages on its own: 20000 keys, d = 64, took 96 us with 8 and 59
+                // with 32, d = 128 74 with 8, 70 with 16 and 73 with 32.  (16-bit
+                // and 8-bit pages, d = 128: 68 us with 8, 80 with 16.)
                 constexpr int TOTAL = 2 * kBlockTokens * VPR, STEP = KS ? 32 : kWarps * 32;
-                constexpr int U = TOTAL / STEP < 8 ? TOTAL / STEP : 8;
+                constexpr int MOST = KS && sizeof(T) == 4 ? (D == 64 ? 32 : 16) : 8;
+                constexpr int U = TOTAL / STEP < MOST ? TOTAL / STEP : MOST;
 #pragma unroll 1
                 for (int i0 = KS ? lane : tid; i0 < TOTAL; i0 += U * STEP) {
                     V v[U];
