@@ -10,10 +10,11 @@
 //                        read from its [key][d] storage as an MN-major operand
 // Two warpgroups of softmax threads, one thread a row, keep the tensor pipe fed:
 // while one turns its S into P, the other's products run.
-//   PAIR   (more than 128 rows): the groups own two row tiles and meet every key
-//          tile together, so K and V are fetched once for 256 rows;
-//   SPLIT  (up to 128 rows): both groups own the same rows and take alternate key
-//          tiles; their two sums are joined at the end from tensor memory.
+//   PAIR   the groups own two row tiles and meet every key tile together, so K and
+//          V are fetched once for 256 rows;
+//   SPLIT  (up to 128 rows, and little work: tile_p) both groups own the same rows
+//          and take alternate key tiles; their two sums are joined at the end from
+//          tensor memory.
 // The maximum m is only moved when a tile exceeds it by more than 2^8 (the
 // weights then stay below 2^8, well inside bf16 and float32), so O is rescaled a
 // few times per row and not per tile.  Weights are rounded to bf16 for the
@@ -1160,8 +1161,24 @@ cudaError_t tile_t(const AttendArgs &a, cudaStream_t s) {
 
 template <int D, bool E4>
 cudaError_t tile_p(const AttendArgs &a, cudaStream_t s) {
-    return (int64_t)a.b.max_q_len * a.gqa > TR ? tile_t<D, E4, true>(a, s)
-                                              : tile_t<D, E4, false>(a, s);
+    // Pairs of row tiles fetch (and convert) K and V once for 256 rows; single row tiles
+    // are passed in half the time, by both groups, and make twice as many pieces of
+    // work.  Those win while there is an SM for each row tile and little work an SM
+    // (as bounded by the batch), us for 8 kv heads of 6 query heads, d = 128:
+    //   tokens, keys     bf16 pair / single      e4m3 pair / single
+    //   32, 1024              20.8 / 15.5            27.2 / 23.1
+    //   32, 4096              21.6 / 17.8            26.4 / 22.7
+    //   256, 1024             22.5 / 16.3            29.4 / 25.3
+    //   256, 2048             28.0 / 23.9            36.0 / 43.4
+    //   256, 4096             36.1 / 39.4            46.5 / 72.9
+    //   512, 1024             22.9 / 39.9            29.9 / 56.1
+    const int64_t of_seq = ((int64_t)a.b.max_q_len * a.gqa + TR - 1) / TR;
+    const int64_t tiles =
+        a.b.G * min(a.b.n_seqs * of_seq, (int64_t)a.b.n_tokens * a.gqa / TR + a.b.n_seqs);
+    const int64_t units = (a.b.max_kv_len + TK - 1) / TK * tiles;
+    const int sms = sm_count();
+    const bool single = of_seq == 1 || (tiles <= sms && units <= (int64_t)sms * (E4 ? 6 : 12));
+    return single ? tile_t<D, E4, false>(a, s) : tile_t<D, E4, true>(a, s);
 }
 
 }  // namespace

@@ -48,6 +48,22 @@ def test_attend_many_tiles(kvm, act, kv, scaled, d, H, q, alike):
     run_attend(kvm, p, True)
 
 
+# Row tiles taken in pairs: more of them than SMs, alike and ragged, the last one of
+# a pair empty or short; and few with so many keys that they are cut and joined.
+@pytest.mark.parametrize("act,kv,scaled", TYPES[:2], ids=IDS[:2])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,G,H", [
+    ([(100, 600)] * 30, 2, 6),
+    ([(1 + (i * 37) % 170, 1 + (i * 211) % 900 + (i * 37) % 170) for i in range(40)], 2, 6),
+    ([(44, 44 + 13 * i) for i in range(60)], 1, 6),
+    ([(700, 5001)], 3, 18),
+    ([(300, 9990), (129, 700), (1, 0)], 4, 8),
+], ids=["alike", "ragged", "short second tile", "cut", "cut and ragged"])
+def test_attend_pairs_of_row_tiles(kvm, act, kv, scaled, d, lens, G, H):
+    p = Paged(lens, G=G, H=H, d=d, kv=kv, act=act, scaled=scaled, seed=d, own_rows=scaled)
+    run_attend(kvm, p, True)
+
+
 @pytest.mark.parametrize("act,kv,scaled", TYPES[:2], ids=IDS[:2])
 def test_attend_many_long_tiles_alike(kvm, act, kv, scaled):
     """More row tiles than CTAs, each of 27 key tiles: runs of parts of a tile."""
