@@ -54,7 +54,7 @@ attend_simt_kernel(AttendArgs a, int min_units) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int cta = blockIdx.x;
     if (warp == 0) {
-        const LineInfo li = W::LN::template lay_out<false>(a, pre, gridDim.x, min_units);
+        const LineInfo li = W::LN::template lay_out<false>(a, pre, gridDim.x, min_units, 2 * min_units);
         if (lane == 0) line = li;
     }
     __syncthreads();

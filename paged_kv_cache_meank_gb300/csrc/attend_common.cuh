@@ -69,7 +69,7 @@ struct Line {
     // their row tiles (pre: kMaxSeqs + 1 in shared memory).  By one warp, a lane to a
     // sequence.
     template <bool PAD>
-    __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units) {
+    __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units, int join) {
         const int lane = threadIdx.x & 31;
         LineInfo li{0, 1, 0, 0};
         int items = 0;
@@ -113,18 +113,17 @@ struct Line {
         }
         if (lane == 0) pre[0] = pre[kMaxSeqs + 1] = 0;
         li.most = __reduce_max_sync(0xffffffffu, li.most);
-        plan<PAD>(li, items, n_ctas, min_units);
+        plan<PAD>(li, items, n_ctas, min_units, join);
         __syncwarp();
         return li;
     }
     // From the row tiles' number, their units and the longest one's: what they are
     // counted as, and the runs.  A join counts as `join` units.
     template <bool PAD>
-    __host__ __device__ static void plan(LineInfo &li, int items, int n_ctas, int min_units) {
+    __host__ __device__ static void plan(LineInfo &li, int items, int n_ctas, int min_units, int join) {
         const int share = (int)(((uint32_t)li.total + n_ctas - 1) / (uint32_t)n_ctas);
-        // below min_units a tile's join costs more than its keys, and a tile of twice
-        // that is not cut
-        const int join = 2 * min_units, least = li.most <= join ? li.most : min_units;
+        // shorter runs than min_units do not pay, and a tile of `join` is not cut
+        const int least = li.most <= join ? li.most : min_units;
         li.per = max(share, least);
         if (!PAD || items == 0) return;
         // A CTA to a tile, and no joins, where the longest takes less longer than an

@@ -45,7 +45,10 @@ constexpr float kMoveMax = 8.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int kMinPages = 8;               // of a CTA's run: below, a join costs more than the keys
+// Pages of a CTA's run at least, and what a join costs.  One sequence of 512, 1024,
+// 2048, 4096 bf16 keys took 6.3, 9.0, 9.4, 9.0 us with 8 and 16; with 4 and 8, 7.6, 7.8,
+// 8.3, 9.2.
+constexpr int kMinPages = 4, kJoinPages = 16;
 
 // W warps a CTA, CTAS of them an SM.
 template <int D, bool E4, int NT, int W, int CTAS>
@@ -128,7 +131,7 @@ __device__ __forceinline__ void e4m3_f16(uint32_t x, uint32_t &lo, uint32_t &hi)
 
 template <int D, bool E4, int NT, int WARPS, int CTAS>
 __global__ void __launch_bounds__(WARPS * 32, CTAS)
-attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
+attend_decode_kernel(const __grid_constant__ AttendArgs a) {
     using LY = Lay<D, E4, NT, WARPS, CTAS>;
     constexpr int RB = LY::RB, KS = D / 16, MT = D / 16, KEYS = LY::KEYS, S = LY::STAGES;
     constexpr int CH = LY::ROW / 16;                       // 16-byte chunks of a row
@@ -142,7 +145,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a, int min_units) {
     const int g8 = lane >> 2, c4 = lane & 3;               // fragment row and column pair
     const int cta = blockIdx.x;
     if (warp == 0) {
-        const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
+        const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, kMinPages, kJoinPages);
         if (lane == 0) line = li;
     }
     __syncthreads();
@@ -650,7 +653,7 @@ cudaError_t decode_t(const AttendArgs &a, cudaStream_t s) {
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = min(LY::MAX_CTAS, CTAS * sm_count());
-    kern<<<ctas, WARPS * 32, LY::SMEM, s>>>(a, kMinPages);
+    kern<<<ctas, WARPS * 32, LY::SMEM, s>>>(a);
     note_launch();
     return cudaGetLastError();
 }

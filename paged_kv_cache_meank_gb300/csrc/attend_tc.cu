@@ -58,9 +58,10 @@ constexpr int HK = TK / 2;                  // keys of half a tile
 constexpr int TR = 128;                     // query rows of a tile
 constexpr int kPagesPerTile = TK / kBlockTokens;
 constexpr uint32_t kWaitNs = 1000000000u;   // 1 s
-// Key tiles of a CTA's run.  With 8, nine ragged sequences of up to 1501 keys took
-// 47.0 us (37.0 with 4) and 32 query tokens over 4096 keys 30.5 (23.7).
-constexpr int kMinTiles = 4;
+// Key tiles of a CTA's run at least, and what a join costs.  32 query tokens over
+// 4096 keys took 18.2 us (e4m3 22.8); with 8 and 16, 22.4 (29.9).  Nine ragged
+// sequences of d = 64 took 25.4, with 2 and 4, or 3 and 6, 34.8.
+constexpr int kMinTiles = 4, kJoinTiles = 8;
 constexpr float kMoveMax = 8.f;             // log2 units a tile may exceed m by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
@@ -285,7 +286,7 @@ __device__ __forceinline__ bool join_rows(const AttendArgs &a, const Seg &sh, in
 template <int D, bool E4, bool PAIR>
 __global__ void __launch_bounds__(Lay<D, E4, PAIR>::THREADS, 1)
 attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ AttendArgs a, int min_units) {
+                   const __grid_constant__ AttendArgs a) {
     using LY = Lay<D, E4, PAIR>;
     constexpr int RB = PAIR ? 2 * TR : TR;
     constexpr int NS = LY::SLOTS, NR = E4 ? LY::RAW_SLOTS : NS;
@@ -562,7 +563,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             using W = Walk<RB, TK>;
             // the prefix sums live in the ring: its first copies follow the first segment
             int *pre = reinterpret_cast<int *>(kvs);
-            const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, min_units);
+            const LineInfo li = W::LN::template lay_out<true>(a, pre, gridDim.x, kMinTiles, kJoinTiles);
             W k;
             bool any = k.start(a, pre, li, blockIdx.x);
             tc::fence_proxy_async_smem();
@@ -1149,9 +1150,8 @@ cudaError_t tile_t(const AttendArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, LY::SMEM);
     if (e != cudaSuccess) return e;
     const int ctas = min(kTileMaxCtas, sm_count());
-    int min_units = kMinTiles;
     AttendArgs args = a;
-    void *params[] = {&kmap, &vmap, &args, &min_units};
+    void *params[] = {&kmap, &vmap, &args};
     // CTAs that share a tile wait for one another at the end: all run at once
     e = cudaLaunchCooperativeKernel((const void *)kern, dim3((unsigned)ctas), dim3(LY::THREADS), params,
                                     LY::SMEM, s);
