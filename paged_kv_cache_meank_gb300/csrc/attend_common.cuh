@@ -66,7 +66,7 @@ struct Line {
         return max(1, (keys(i, a, r) + UNIT - 1) / UNIT);
     }
     // Lays the line out: pre[s] = units of the sequences before s, or with `pad`
-    // their row tiles (pre: kMaxSeqs + 1 in shared memory).  By one warp, a lane to a
+    // their row tiles (pre: kPreInts in shared memory).  By one warp, a lane to a
     // sequence.
     template <bool PAD>
     __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units, int join) {
