@@ -235,9 +235,9 @@ struct BatchArgs {
     int L, G, layer;
     int *err;
 };
-// Raised in the device error word by the batch kernels.
-constexpr int kErrBatch = 8;       // a length, page, scale row or position out of range
-constexpr int kErrScale = 16;      // a scale that is not a power of two in range
+// Raised in the device error word by the batch kernels: a length, page, scale row
+// or position out of range.  (16: a scale that is no power of two, checked_scale.)
+constexpr int kErrBatch = 8;
 
 constexpr int kMaxSeqs = 1024;
 
