@@ -554,6 +554,9 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * over e4m3 pages each weight times its v_scale is rounded to float16 against the
  * largest such product of its row (below 2^-14 of it the rounding is absolute,
  * 2^-25 of it at most).  Every other pairing of types runs in float32 throughout.
+ * As float32 has it, weights below 2^-110 of their row's largest may count for less
+ * whatever their v, and sums of weighted values run unnormalised: the largest |v|
+ * times the number of keys stays below 2^119.
  * Results do not depend on the order in which parts of the work end: the same
  * call gives the same bits.
  * Cache rows at or behind kv_len are not read into the result whatever they

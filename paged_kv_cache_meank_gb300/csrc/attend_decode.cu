@@ -18,7 +18,7 @@
 //
 // e4m3: as in attend_tc.cu codes become f16 (exact) in registers, q is divided by
 // a power of two per row, the page's k_scale goes into the factor of the scores
-// and the weights times v_scale have a running maximum of their own.
+// and the weights times v_scale, by a finite factor, have a running maximum of their own.
 //
 // One sequence of 32768 bf16 keys takes 26.9 us, 19.0 of them its 134 MB at the
 // 7.06 TB/s that longer sequences add; the start (lengths, page numbers and keys,
@@ -41,7 +41,7 @@ namespace kvm {
 
 namespace {
 
-constexpr float kMoveMax = 8.f;
+constexpr float kMoveMax = 8.f, kMostW = 127.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -411,7 +411,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     base[b] = m[t][b] == -INFINITY ? 0.f : m[t][b];
-                    w[b] = !E4 ? 1.f : m[t][b] == -INFINITY ? 0.f : ex2(lv + m[t][b] - mp[t][b]);
+                    w[b] = !E4 ? 1.f : m[t][b] == -INFINITY ? 0.f : ex2(fminf(lv + m[t][b] - mp[t][b], kMostW));
                 }
 #pragma unroll
                 for (int u = 0; u < KEYS / 16; ++u) {

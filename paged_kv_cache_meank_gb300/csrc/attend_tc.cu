@@ -24,7 +24,9 @@
 // tiles in f16 (exact, one instruction for two codes), and the products run in
 // f16.  q is divided by a power of two per row first; k_scale goes into the
 // factor of the page's scores; the weights times v_scale are kept in f16 against a
-// running maximum of their own, so scales of any size keep their precision.
+// running maximum of their own, 2^mp.  A weight p = 2^(x - m) becomes p w, w =
+// 2^(log2 v_scale + m - mp); as p w is at most 2^8, a w beyond float32 only meets
+// weights below 2^-110, and is bounded (a masked p of 0 times infinity is no number).
 //
 // Warps: 0 TMA producer, 1 and 3 MMA issuers (one for each group), 2 walks the
 // CTA's run of the work line and hands its segments to the others, 4-7 and 8-11
@@ -63,6 +65,7 @@ constexpr uint32_t kWaitNs = 1000000000u;   // 1 s
 // sequences of d = 64 took 25.4, with 2 and 4, or 3 and 6, 34.8.
 constexpr int kMinTiles = 4, kJoinTiles = 8;
 constexpr float kMoveMax = 8.f;             // log2 units a tile may exceed m by
+constexpr float kMostW = 127.f;             // log2 of the largest w
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
 constexpr float kLn2 = 0.6931471805599453f;
@@ -768,7 +771,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 // E4: from weights to what multiplies V's codes
-                                const float w = E4 && m != -INFINITY ? ex2(lv[y] + m - mp) : 0.f;
+                                const float w = E4 && m != -INFINITY ? ex2(fminf(lv[y] + m - mp, kMostW)) : 0.f;
                                 uint32_t p[16];
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {

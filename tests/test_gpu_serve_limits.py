@@ -1,0 +1,146 @@
+"""kvm_attend, kvm_append_kv and kvm_build_index_scaled at the limits of what their
+documentation allows: scales far apart, weights far apart, entries that are not
+finite, stored scales that are no scales, buffers in host memory, waits that give
+up.  Against the 64-bit definitions of serve_ref; what a test adds to its
+tolerances is derived in place."""
+import math
+
+import pytest
+import torch
+
+import serve_ref as ref
+from serve_ref import EPS2, TDT, U, Paged
+from test_gpu_serve import context, kvm   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(kvm, p, scale, causal=True):
+    """One call: (out, lse) in 64 bits on the host."""
+    ctx = context(kvm, L=p.L, G=p.G, H=p.H, d=p.d, kv=p.kv, act=p.act)
+    batch, cache = p.on(ctx)
+    out = torch.full((p.n, p.H, p.d), 7.0, device="cuda").to(TDT[p.act])
+    lse = torch.full((p.n, p.H), 7.0, device="cuda")
+    ctx.attend(batch, cache, p.layer, p.q.cuda(), out, lse=lse, scale=scale, causal=causal)
+    ctx.sync()
+    return out.cpu().double(), lse.cpu().double()
+
+
+def products(p, scale, lse):
+    """For every query row: the largest of its weights times v_scale, the sum of the
+    |codes| it sees, and what weights below 2^-110 of its largest give, which may
+    count for less: [n, H], [n, H, d] twice."""
+    top = torch.zeros(p.n, p.H, dtype=torch.float64)
+    codes = torch.zeros(p.n, p.H, p.d, dtype=torch.float64)
+    faint = torch.zeros_like(codes)
+    r = p.H // p.G
+    for s, (qn, kvl) in enumerate(p.lens):
+        at = slice(p.q_start[s], p.q_start[s] + qn)
+        rows = (p.rows if p.rows is not None else p.table)[s, :-(-kvl // 32)].long()
+        seen = torch.arange(kvl)[None, :] <= kvl - qn + torch.arange(qn)[:, None]
+        for g in range(p.G):
+            k, v = p.heads(s, g)
+            vs = p.vs[rows, p.layer, g].double().repeat_interleave(32)[:kvl]
+            h = slice(g * r, (g + 1) * r)
+            x = torch.einsum("nhd,kd->nhk", p.q[at, h].double(), k) * scale - lse[at, h][..., None]
+            w = torch.where(seen[:, None], torch.exp(torch.where(seen[:, None], x, 0.0)), 0.0)
+            small = torch.where(w < 2.0 ** -110 * w.amax(-1, keepdim=True), w, 0.0)
+            faint[at, h] = torch.einsum("nhk,kd->nhd", small, v.abs())
+            top[at, h] = (w * vs).amax(-1)
+            codes[at, h] = torch.einsum("nk,kd->nd", seen.double(), (v / vs[:, None]).abs())[:, None]
+    return top, codes, faint
+
+
+def check_scaled(p, scale, out, lse, bits):
+    """Against the 64-bit attention.  The e4m3 form holds a weight times its v_scale
+    as a 16-bit float whose rounding is at most 2^-(bits + 1) of the row's largest such
+    product, 2^-bits with that maximum itself up to one float32 rounding off;
+    a key adds that times its code to the sum."""
+    want, wl, absv, ds = p.reference(scale, True)
+    top, codes, faint = products(p, scale, wl)
+    lost = 2.0 ** -bits * top[..., None] * codes
+    assert bool(torch.isfinite(out).all())
+    err = (out - want).abs()
+    tol = ref.attend_tolerance(want, absv, ds, p.act, p.kv, p.max_kv) + lost + faint
+    assert (err <= tol).all(), f"worst error / tolerance {(err / tol).max():.3g}"
+    assert torch.equal(lse == -math.inf, wl == -math.inf)
+    tl = ds * 2 + (p.max_kv + 16) * U + 4 * U * wl.abs()
+    assert ((lse - wl).abs() <= tl).all()
+
+
+# One sequence, several, more row tiles than SMs: the forms for a decoded token (with
+# eight warps and with four), for one row tile and for pairs of them.
+FORMS = {"decode": ([2], 1), "decode, many": ([2] * 90, 2), "tile": ([40], 1), "pairs": ([100] * 30, 2)}
+
+
+# ---------------------------------------------------------------- scales far apart
+
+def far_apart(form, n_keys, seed):
+    lens, G = FORMS[form]
+    return Paged([(q, n_keys) for q in lens], G=G, H=6 * G, d=64, kv="e4m3", act="bf16", scaled=True,
+                 seed=seed)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("exponent", [20, 28, 30, 64, 105])
+def test_attend_masked_page_of_a_far_larger_scale(kvm, form, exponent):
+    """Rows that see only pages whose v_scale is the least there is, beside a page
+    that they do not see, whose scale is 2^128 and more times that."""
+    p = far_apart(form, 289, 1)                          # the last page: one key, seen by the last token
+    for s in range(len(p.lens)):
+        pages = p.table[s, :10].long()
+        p.vs[pages] = 2.0 ** -100
+        p.vs[pages[9]] = 2.0 ** exponent
+    scale = p.d ** -0.5
+    check_scaled(p, scale, *attend(kvm, p, scale), 24)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("gap,low,high", [(60, -40, 100), (100, -100, 40), (109, -100, 100), (126.5, -100, 27),
+                                          (127, -100, 27), (127.5, -100, 28), (130, -100, 40), (140, -100, 100),
+                                          (180, -100, 105)])
+@pytest.mark.parametrize("first", [True, False], ids=["early", "late"])
+def test_attend_small_weights_of_a_far_larger_scale(kvm, form, gap, low, high, first):
+    """Half the pages score `gap` (log2) above the other half and have v_scale
+    2^low, the other half 2^high: a weight of 2^-gap, which float32 may not hold, times
+    a scale that brings it back into the result."""
+    p = far_apart(form, 512, 2)
+    scale = gap * math.log(2) / 128                      # q.k = +-64
+    p.q[:] = 1.0
+    p.ks[:] = 1.0
+    one = torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    for s in range(len(p.lens)):
+        pages = p.table[s, :16].long()
+        top = pages[:8] if first else pages[8:]
+        p.k[pages] = one | 0x80
+        p.k[top] = one
+        p.vs[pages] = 2.0 ** high
+        p.vs[top] = 2.0 ** low
+    check_scaled(p, scale, *attend(kvm, p, scale), 24)
+
+
+@pytest.mark.parametrize("q,kv_len", [(2, 33), (64, 64)], ids=["decode", "tile"])
+def test_attend_after_a_block_of_zeros(kvm, q, kv_len):
+    """V of the first block all zeros (kvm_append_kv gives it the least scale), of the
+    next 1e12: a token of the first block gets zeros."""
+    G, H, d = 2, 12, 128
+    ctx = context(kvm, L=1, G=G, H=H, d=d, kv="e4m3", act="bf16")
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn(kv_len, G, d, generator=g).bfloat16()
+    v = torch.zeros(kv_len, G, d).bfloat16()
+    v[32:] = 1e12
+    kp, vp = (torch.zeros(2, 1, G, 32, d, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(2, 1, G, device="cuda") for _ in range(2))
+    cache = ctx.cache(kp, vp, ks, vs)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")     # noqa: E731
+    table = i32([[1, 0]])
+    ctx.append_kv(ctx.batch(i32([0, kv_len]), i32([kv_len]), table, n_tokens=kv_len, max_q_len=kv_len,
+                            max_kv_len=64), cache, 0, k.cuda(), v.cuda())
+    batch = ctx.batch(i32([0, q]), i32([kv_len]), table, n_tokens=q, max_q_len=q, max_kv_len=64)
+    out = torch.full((q, H, d), 7.0, device="cuda").bfloat16()
+    ctx.attend(batch, cache, 0, torch.randn(q, H, d, generator=g).bfloat16().cuda(), out)
+    ctx.sync()
+    assert float(vs[1, 0, 0]) == 2.0 ** -100
+    first = 32 - (kv_len - q)                            # tokens of the first block
+    assert (out[:first] == 0).all()
+    assert torch.isfinite(out).all() and (out[first:] > 0).all()
