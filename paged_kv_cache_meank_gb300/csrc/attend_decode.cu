@@ -18,7 +18,7 @@
 //
 // e4m3: as in attend_tc.cu codes become f16 (exact) in registers, q is divided by
 // a power of two per row, the page's k_scale goes into the factor of the scores
-// and the weights times v_scale, by a finite factor, have a running maximum of their own.
+// and the weights times v_scale, by a finite factor, have a reference of their own.
 //
 // One sequence of 32768 bf16 keys takes 26.9 us, 19.0 of them its 134 MB at the
 // 7.06 TB/s that longer sequences add; the start (lengths, page numbers and keys,
@@ -41,7 +41,7 @@ namespace kvm {
 
 namespace {
 
-constexpr float kMoveMax = 8.f, kMostW = 127.f;
+constexpr float kMoveMax = 8.f, kUp = 7.f, kMostW = 127.f;   // (as in attend_tc.cu)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -376,7 +376,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                             top = fmaxf(top, x);
                         }
                     // (a first finite score exceeds the m of -infinity)
-                    grow |= top > m[t][b] + kMoveMax || (E4 && top + lv > mp[t][b] + kMoveMax);
+                    grow |= top > m[t][b] + kMoveMax || (E4 && top + (lv - kUp) > mp[t][b] + kMoveMax);
                 }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -389,7 +389,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1)
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                        const float mn = fmaxf(m[t][b], x), mpn = E4 ? fmaxf(mp[t][b], x + lv) : mn;
+                        const float mn = fmaxf(m[t][b], x), mpn = E4 ? fmaxf(mp[t][b], x + (lv - kUp)) : mn;
                         const bool none = m[t][b] == -INFINITY;
                         const float f = none ? 0.f : ex2(m[t][b] - mn);
                         const float fp = E4 ? (none ? 0.f : ex2(mp[t][b] - mpn)) : f;

@@ -24,9 +24,12 @@
 // tiles in f16 (exact, one instruction for two codes), and the products run in
 // f16.  q is divided by a power of two per row first; k_scale goes into the
 // factor of the page's scores; the weights times v_scale are kept in f16 against a
-// running maximum of their own, 2^mp.  A weight p = 2^(x - m) becomes p w, w =
-// 2^(log2 v_scale + m - mp); as p w is at most 2^8, a w beyond float32 only meets
-// weights below 2^-110, and is bounded (a masked p of 0 times infinity is no number).
+// reference of their own, 2^mp.  A weight p = 2^(x - m) becomes p w, w = 2^(log2
+// v_scale + m - mp).  mp is kUp below the running maximum: p w is at most 2^(8 + 7), just
+// inside f16, and the room is at its lower end, where many small weights can add up
+// (what it rounds away is at most 2^-32 of the row's largest p w).  A w beyond float32
+// only meets weights below 2^-110, and is bounded (a masked p of 0 times infinity is no
+// number).
 //
 // Warps: 0 TMA producer, 1 and 3 MMA issuers (one for each group), 2 walks the
 // CTA's run of the work line and hands its segments to the others, 4-7 and 8-11
@@ -65,6 +68,7 @@ constexpr uint32_t kWaitNs = 1000000000u;   // 1 s
 // sequences of d = 64 took 25.4, with 2 and 4, or 3 and 6, 34.8.
 constexpr int kMinTiles = 4, kJoinTiles = 8;
 constexpr float kMoveMax = 8.f;             // log2 units a tile may exceed m by
+constexpr float kUp = 7.f;
 constexpr float kMostW = 127.f;             // log2 of the largest w
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
@@ -808,7 +812,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         if constexpr (E4) {
                             const float x0 = top0 * kc[0], x1 = top1 * kc[1];
                             m_new = fmaxf(m, fmaxf(x0, x1));
-                            mp_new = fmaxf(mp, fmaxf(x0 + lv[0], x1 + lv[1]));
+                            mp_new = fmaxf(mp, fmaxf(x0 + lv[0], x1 + lv[1]) - kUp);
                             grow = m_new > m + kMoveMax || mp_new > mp + kMoveMax;
                         } else {
                             m_new = mp_new = fmaxf(m, fmaxf(top0, top1) * c);

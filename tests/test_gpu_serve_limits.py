@@ -144,3 +144,26 @@ def test_attend_after_a_block_of_zeros(kvm, q, kv_len):
     first = 32 - (kv_len - q)                            # tokens of the first block
     assert (out[:first] == 0).all()
     assert torch.isfinite(out).all() and (out[first:] > 0).all()
+
+
+# ---------------------------------------------------------------- weights far apart
+
+@pytest.mark.parametrize("q", [1, 20, 40])
+@pytest.mark.parametrize("below", [22.3, 25.4, 26.5])
+def test_attend_flat_tail_far_below_the_largest_weight(kvm, q, below):
+    """One key takes all but 2^-below n of the weight and has V = 0: what is left is
+    the sum of many products far below the row's largest."""
+    kv_len = 6000
+    p = Paged([(q, kv_len)], G=1, H=6, d=64, kv="e4m3", act="bf16", scaled=True, seed=3)
+    scale = below * math.log(2) / 128                    # q.k = +-64
+    one = torch.tensor(1.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    p.q[:] = 1.0
+    p.ks[:] = 1.0
+    p.vs[:] = 0.25
+    p.k[:] = one | 0x80
+    p.v[p.v == 0x7F] = 0x30
+    p.v &= 0x7F                                          # all of one sign: nothing cancels
+    page = int(p.table[0, 40])
+    p.k[page, 0, 0, 7] = one
+    p.v[page, 0, 0, 7] = 0
+    check_scaled(p, scale, *attend(kvm, p, scale), 31)
