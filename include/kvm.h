@@ -553,7 +553,8 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * sums in float32, with the weights rounded to bf16 before the product with V;
  * over e4m3 pages each weight times its v_scale is rounded to float16 against the
  * largest such product of its row (below 2^-21 of it the rounding is absolute,
- * 2^-32 of it at most).  Every other pairing of types runs in float32 throughout.
+ * 2^-32 of it at most), and query entries below 2^-32 of their row's largest are
+ * rounded to 2^-39 of it.  Every other pairing of types runs in float32 throughout.
  * As float32 has it, weights below 2^-110 of their row's largest may count for less
  * whatever their v, and sums of weighted values run unnormalised: the largest |v|
  * times the number of keys stays below 2^119.

@@ -259,9 +259,8 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                 }
                 e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
                 e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-                // the row's largest entry into [1, 2), within what 2^-x and 2^x allow; none
-                // for a row of zeros
-                const int x = e == 0 ? 0 : min(126, max(-126, (int)(e >> 7) - 127));
+                // the row's largest entry into [2^15, 2^16), as row_exponent in attend_tc.cu
+                const int x = min(127, max(-101, (int)(e >> 7) - 127)) - 15;
                 const float dn = __uint_as_float((uint32_t)(127 - x) << 23);
                 const float up = __uint_as_float((uint32_t)(127 + x) << 23);
 #pragma unroll

@@ -22,7 +22,7 @@
 //
 // e4m3 pages: a fourth warpgroup turns each page's codes into the same swizzled
 // tiles in f16 (exact, one instruction for two codes), and the products run in
-// f16.  q is divided by a power of two per row first; k_scale goes into the
+// f16.  q is divided by a power of two per row first (row_exponent); k_scale goes into the
 // factor of the page's scores; the weights times v_scale are kept in f16 against a
 // reference of their own, 2^mp.  A weight p = 2^(x - m) becomes p w, w = 2^(log2
 // v_scale + m - mp).  mp is kUp below the running maximum: p w is at most 2^(8 + 7), just
@@ -186,8 +186,10 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there
 }
 
 // The largest biased exponent of 8 bf16, and the power of two that a query row
-// with that largest exponent is divided by on its way to f16 (kept where it and
-// its inverse are normal float32; none for a row of zeros).
+// with that largest exponent is divided by on its way to f16: its largest entry comes
+// into [2^15, 2^16), the top of f16 (65504; a bf16 has 8 bits, 65280 is the most),
+// so that entries down to 2^-32 of it are exact.  Kept where the factors of its
+// scores stay normal float32.
 __device__ __forceinline__ int max_exponent(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t e = 0;
@@ -196,7 +198,7 @@ __device__ __forceinline__ int max_exponent(uint4 v) {
     return (int)(e >> 7);
 }
 __device__ __forceinline__ int row_exponent(int biased) {
-    return biased == 0 ? 0 : min(126, max(-126, biased - 127));
+    return min(127, max(-101, biased - 127)) - 15;
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ uint32_t f16_of_bf16(uint32_t two, float f) {
@@ -664,8 +666,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     }
                     asm volatile("cp.async.wait_all;" ::: "memory");
                     if (E4 || flip || !keep) {
-                        // each thread's own chunks: the scale's sign; E4: to f16, the row's
-                        // largest entry in [1, 2)
+                        // each thread's own chunks: the scale's sign; E4: to f16
                         constexpr int B = 4;
 #pragma unroll 1
                         for (int i0 = 0; i0 < N; i0 += B) {

@@ -167,3 +167,28 @@ def test_attend_flat_tail_far_below_the_largest_weight(kvm, q, below):
     p.k[page, 0, 0, 7] = one
     p.v[page, 0, 0, 7] = 0
     check_scaled(p, scale, *attend(kvm, p, scale), 31)
+
+
+@pytest.mark.parametrize("q", [2, 40])
+@pytest.mark.parametrize("size", [-16, -20, -27])
+def test_attend_query_rows_of_one_large_entry(kvm, q, size):
+    """Query entries 2^size of their row's largest, which meets zeros in K: the
+    scores are made of the small ones alone."""
+    p = Paged([(q, 200), (q, 77)], G=1, H=6, d=64, kv="e4m3", act="bf16", scaled=True, seed=4)
+    p.q = (p.q.double() * 2.0 ** size).bfloat16()
+    p.q[:, :, 5] = 1.5
+    p.k[..., 5] = 0
+    p.ks[:] = 2.0 ** (-6 - size)
+    check_scaled(p, 64 ** -0.5, *attend(kvm, p, 64 ** -0.5), 24)
+
+
+@pytest.mark.parametrize("q", [2, 40])
+@pytest.mark.parametrize("size", [-100, -112, -120, -130, 60, 100, 119, 125])
+def test_attend_query_rows_of_any_size(kvm, q, size):
+    """Rows as small as bf16 has them, subnormal entries among them, and as large,
+    against K whose scale makes up for it where the range of scales allows."""
+    p = Paged([(q, 200), (q, 77)], G=1, H=6, d=64, kv="e4m3", act="bf16", scaled=True, seed=5)
+    p.q = (p.q.double() * 2.0 ** size).bfloat16()
+    p.ks[:] = 2.0 ** max(-100, min(119, -6 - size))
+    scale = 64 ** -0.5 * 2.0 ** (-6 - size - max(-100, min(119, -6 - size)))
+    check_scaled(p, scale, *attend(kvm, p, scale), 24)
