@@ -11,10 +11,11 @@
  * read or write may be device memory or pinned (page-locked) host memory; the
  * kernels then access pinned host memory directly over the host link, moving
  * only the bytes they touch.  Pageable host memory is rejected
- * (KVM_ERR_INVALID_ARG).  The one exception is the Mean-K index read by
+ * (KVM_ERR_INVALID_ARG).  There are two exceptions.  The Mean-K index read by
  * kvm_score_select: with index_location KVM_DEVICE it must be device memory
  * (TMA streams it), and with KVM_HOST_PINNED it is pinned host memory staged
- * in tiles.  All work is enqueued on the caller's stream;
+ * in tiles.  The buffers of kvm_qk_norm_rope, kvm_append_kv and kvm_attend: all
+ * are device memory.  All work is enqueued on the caller's stream;
  * functions return after enqueueing unless stated otherwise.  No C++
  * exception crosses this boundary: every function returns a kvm_status.
  * Argument errors are detected on the host before anything is enqueued and
@@ -581,8 +582,11 @@ kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cac
  * un-rotated codes (rounded once), and raw_k_out (nullable) takes the un-rotated
  * codes, which keep the pages' scales.
  * k_scale  device [n_blocks][L][G] float32: row i belongs to k_pages block i.
+ * Every buffer, k_scale too, may lie in pinned host memory, as with
+ * kvm_build_index (an index with index_location KVM_HOST_PINNED does).
  * Everything else, errors included, as kvm_build_index; KVM_ERR_INVALID_ARG
- * unless kv_dtype is KVM_E4M3.
+ * unless kv_dtype is KVM_E4M3, or where k_pages, index or raw_k_out is not aligned to
+ * 16 bytes.
  */
 kvm_status kvm_build_index_scaled(kvm_ctx *ctx, const void *k_pages, const float *k_scale,
                                   int64_t first_block, int64_t n_blocks, void *index,

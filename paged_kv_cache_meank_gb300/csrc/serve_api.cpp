@@ -28,14 +28,19 @@ kvm_status launched(cudaError_t e, const char *what) {
 
 int64_t elt_bytes(int dt) { return dt == KVM_E4M3 ? 1 : dt == KVM_BF16 ? 2 : 4; }
 
-// A buffer of these calls: device memory of the context's device (managed
-// memory counts), 16-byte aligned where `vec`.
-kvm_status on_device(const void *p, const kvm::CtxView &c, const char *what, bool vec = true) {
-    if (!p) return KVM_OK;
+kvm_status aligned(const void *p, const char *what, bool vec) {
     if (vec && ((uintptr_t)p & 15) != 0)
         return fail(KVM_ERR_INVALID_ARG, "%s: not 16-byte aligned", what);
     if (!vec && ((uintptr_t)p & 3) != 0)
         return fail(KVM_ERR_INVALID_ARG, "%s: not 4-byte aligned", what);
+    return KVM_OK;
+}
+
+// A buffer of these calls: device memory of the context's device (managed
+// memory counts), 16-byte aligned where `vec`.
+kvm_status on_device(const void *p, const kvm::CtxView &c, const char *what, bool vec = true) {
+    if (!p) return KVM_OK;
+    if (const kvm_status st = aligned(p, what, vec); st != KVM_OK) return st;
     cudaPointerAttributes a{};
     if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
         cudaGetLastError();
@@ -48,6 +53,12 @@ kvm_status on_device(const void *p, const kvm::CtxView &c, const char *what, boo
         return fail(KVM_ERR_INVALID_ARG, "%s: memory of device %d, the context's is %d", what,
                     a.device, c.device);
     return KVM_OK;
+}
+
+// A buffer that may be pinned host memory too: the address a kernel uses.
+kvm_status kernel_buffer(const void *p, const void **out, const char *what, bool vec = true) {
+    if (const kvm_status st = aligned(p, what, vec); st != KVM_OK) return st;
+    return static_cast<kvm_status>(kvm::resolve_kernel_ptr(p, out, what));
 }
 
 // The context's device has to be the current one: the launches go there.
@@ -313,13 +324,16 @@ kvm_status kvm_build_index_scaled(kvm_ctx *ctx, const void *k_pages, const float
                     (long long)c.max_positions);
     if (n_blocks == 0) return KVM_OK;
     KVM_TRY(current_device(c));
-    KVM_TRY(on_device(k_pages, c, "k_pages"));
-    KVM_TRY(on_device(k_scale, c, "k_scale", false));
-    KVM_TRY(on_device(index, c, "index"));
-    KVM_TRY(on_device(raw_k_out, c, "raw_k_out"));
+    // buffers as kvm_build_index takes them: pinned host memory too
+    const void *pages, *scales, *idx, *raw;
+    KVM_TRY(kernel_buffer(k_pages, &pages, "k_pages"));
+    KVM_TRY(kernel_buffer(k_scale, &scales, "k_scale", false));
+    KVM_TRY(kernel_buffer(index, &idx, "index"));
+    KVM_TRY(kernel_buffer(raw_k_out, &raw, "raw_k_out"));
     return launched(
-        kvm::launch_meank_scaled(c.index_dtype, c.d, k_pages, k_scale, raw_k_out, index,
-                                 c.max_blocks, first_block, n_blocks, c.L * c.G, c.table, c.err,
+        kvm::launch_meank_scaled(c.index_dtype, c.d, pages, static_cast<const float *>(scales),
+                                 const_cast<void *>(raw), const_cast<void *>(idx), c.max_blocks,
+                                 first_block, n_blocks, c.L * c.G, c.table, c.err,
                                  reinterpret_cast<cudaStream_t>(stream)),
         "scaled meank launch");
 }

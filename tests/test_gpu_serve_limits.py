@@ -192,3 +192,32 @@ def test_attend_query_rows_of_any_size(kvm, q, size):
     p.ks[:] = 2.0 ** max(-100, min(119, -6 - size))
     scale = 64 ** -0.5 * 2.0 ** (-6 - size - max(-100, min(119, -6 - size)))
     check_scaled(p, scale, *attend(kvm, p, scale), 24)
+
+
+# ---------------------------------------------------------------- the index of scaled pages
+
+def test_index_of_scaled_pages_in_host_memory(kvm):
+    """Buffers where kvm_build_index takes them: pinned host memory too (an index with
+    index_location KVM_HOST_PINNED lives there)."""
+    wl = ref.workload(L=2, G=3, H=3, d=64, kv="e4m3", act="bf16", index="bf16", n_blocks=64, theta=1e6)
+    ctx = kvm.Context(kvm.config_for(wl))
+    g = torch.Generator().manual_seed(6)
+    n, first = 7, 9
+    codes = (torch.randn(n, 2, 3, 32, 64, generator=g) * 60).to(torch.float8_e4m3fn).view(torch.uint8)
+    ks = torch.exp2(torch.randint(-9, 4, (n, 2, 3), generator=g).float())
+    index, raw = torch.zeros(ctx.index_shape(), dtype=torch.bfloat16), torch.zeros_like(codes)
+    got = [t.cuda() for t in (index, raw)]
+    ctx.build_index(codes.cuda(), first, n, got[0], got[1], k_scale=ks.cuda())
+    host = [t.pin_memory() for t in (codes, index, raw, ks)]
+    ctx.build_index(host[0], first, n, host[1], host[2], k_scale=host[3])
+    ctx.sync()
+    assert host[1].any() and torch.equal(host[1], got[0].cpu()) and torch.equal(host[2], got[1].cpu())
+    plain = [t.pin_memory() for t in (index, raw)]
+    ctx.build_index(host[0], first, n, plain[0], plain[1])          # the call it follows
+    ctx.sync()
+    assert torch.equal(plain[1], host[2])
+    for bad in ((codes, host[1]), (host[0], index)):                # pageable memory
+        with pytest.raises(kvm.KvmError) as e:
+            ctx.build_index(bad[0], first, n, bad[1], k_scale=host[3])
+        assert e.value.name == "KVM_ERR_INVALID_ARG"
+    ctx.close()
