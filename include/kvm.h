@@ -525,6 +525,8 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
  * rows before the first written one follow by the power of two (exact, but for
  * entries that become subnormal, which round to nearest even).  Entries that
  * are not finite do not set the scale: infinities saturate, NaN stays.
+ * A block to be continued whose k_scale or v_scale so far is no such power of two
+ * raises the device error flag; its head's codes and scales are left as they were.
  * Each page written belongs to one sequence of the batch; a sequence with
  * kv_len < q_len raises the device error flag and is skipped.
  * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences or

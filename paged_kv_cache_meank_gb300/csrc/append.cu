@@ -97,8 +97,11 @@ append_kernel(AppendArgs a, int spans) {
 
     float inv = 1.f;
     if constexpr (SCALED) {
-        float *sp = (is_k ? a.k_scale : a.v_scale) + ((size_t)srow * a.b.L + a.b.layer) * a.b.G + g;
-        const float old = r0 > 0 ? *sp : 0.f;           // read by all before one writes
+        const size_t so = ((size_t)srow * a.b.L + a.b.layer) * a.b.G + g;
+        float *sp = (is_k ? a.k_scale : a.v_scale) + so;
+        // read by all before one writes; K's and V's, as the block is left as it was where
+        // either is no scale
+        const float old_k = r0 > 0 ? a.k_scale[so] : 1.f, old_v = r0 > 0 ? a.v_scale[so] : 1.f;
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
@@ -118,11 +121,15 @@ append_kernel(AppendArgs a, int spans) {
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         if (lane == 0) top[warp] = amax;
         if (!__syncthreads_or(on != 0)) return;         // (K's and V's positions are the same)
+        if (!is_scale(old_k) || !is_scale(old_v)) {     // (the same for all)
+            if (threadIdx.x == 0) atomicOr(a.b.err, kErrScale);
+            return;
+        }
 #pragma unroll
         for (int w = 0; w < kParts; ++w) amax = fmaxf(amax, top[warp - part + w]);
         float scale = pow2f(scale_exponent(amax, is_k ? kMostK : kMostV));
         if (r0 > 0) {
-            const float had = checked_scale(old, a.b.err);
+            const float had = is_k ? old_k : old_v;
             if (had >= scale) {
                 scale = had;
             } else {

@@ -236,7 +236,7 @@ struct BatchArgs {
     int *err;
 };
 // Raised in the device error word by the batch kernels: a length, page, scale row
-// or position out of range.  (16: a scale that is no power of two, checked_scale.)
+// or position out of range.  (A scale that is none: kErrScale, kvm_vec.cuh.)
 constexpr int kErrBatch = 8;
 
 constexpr int kMaxSeqs = 1024;

@@ -146,11 +146,14 @@ __device__ inline void store_n(T *p, const float (&f)[N]) {
     }
 }
 
-// A block's scale as read: a power of two 2^e with -100 <= e <= 119, or the
-// device error flag (bit 16) is raised.
-__device__ inline float checked_scale(float s, int *err) {
+// A block's scale: a power of two 2^e with -100 <= e <= 119.
+__device__ inline bool is_scale(float s) {
     const uint32_t u = __float_as_uint(s);
-    if ((u & 0x807FFFFFu) != 0 || (u >> 23) - 27u > 219u) atomicOr(err, 16);
+    return (u & 0x807FFFFFu) == 0 && (u >> 23) - 27u <= 219u;
+}
+constexpr int kErrScale = 16;   // raised in the device error word: a scale that is none
+__device__ inline float checked_scale(float s, int *err) {
+    if (!is_scale(s)) atomicOr(err, kErrScale);
     return s;
 }
 

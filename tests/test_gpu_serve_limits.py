@@ -221,3 +221,39 @@ def test_index_of_scaled_pages_in_host_memory(kvm):
             ctx.build_index(bad[0], first, n, bad[1], k_scale=host[3])
         assert e.value.name == "KVM_ERR_INVALID_ARG"
     ctx.close()
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("side", ["k", "v"])
+@pytest.mark.parametrize("bad", [0.0, math.nan, 0.3, -0.5, math.inf, 2.0 ** -110, 2.0 ** 120])
+def test_append_behind_a_stored_scale_that_is_none(kvm, side, bad):
+    """A block whose stored scale is no allowed power of two: the flag is raised, its
+    codes and scales stay (of K, V and raw K), the other heads and blocks are
+    appended to."""
+    G, d = 3, 64
+    ctx = context(kvm, L=1, G=G, H=6, d=d, kv="e4m3", act="bf16")
+    p = Paged([(40, 50), (2, 70)], G=G, H=6, d=d, kv="e4m3", act="bf16", scaled=True, seed=7, own_rows=True)
+    x = torch.randn(42, G, d, generator=torch.Generator().manual_seed(8)).bfloat16().cuda() * 1000
+    after = []
+    for spoil in (False, True):
+        batch, cache = p.on(ctx)                          # fresh copies
+        raw = torch.full_like(p.dk, 0x21)
+        if spoil:
+            row = int(p.rows[0, 0])
+            (p.dks if side == "k" else p.dvs)[row, 0, 1] = bad
+        before = [t.clone() for t in (p.dk, p.dv, raw, p.dks, p.dvs)]
+        ctx.append_kv(batch, cache, 0, x, x, raw_k_pages=raw)
+        if spoil:
+            with pytest.raises(kvm.KvmError) as e:
+                ctx.sync()
+            assert e.value.name == "KVM_ERR_DEVICE"
+        ctx.sync()
+        after.append([t.clone() for t in (p.dk, p.dv, raw, p.dks, p.dvs)])
+    page = int(p.table[0, 0])
+    for i, (good, got, was) in enumerate(zip(*after, before)):
+        at = (page, 0, 1) if i < 3 else (row, 0, 1)
+        bits = (lambda t: t) if i < 3 else (lambda t: t.view(torch.int32))     # noqa: E731
+        assert torch.equal(bits(got)[at], bits(was)[at]), "the block and head of the bad scale"
+        good[at] = got[at]
+        assert torch.equal(bits(got), bits(good)), "everything else"
