@@ -524,7 +524,10 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
  * every position, and raw K shares it.  Where the scale grows, the codes of the
  * rows before the first written one follow by the power of two (exact, but for
  * entries that become subnormal, which round to nearest even).  Entries that
- * are not finite do not set the scale: infinities saturate, NaN stays.
+ * are not finite do not set the scale: an infinity counts as 448 times it, before
+ * the rotation too; NaN stays (and reaches its partner in K's rotated row).
+ * Without scales infinities go through the rotation as float32 has it, where
+ * infinity times a sine of 0 is NaN.
  * A block to be continued whose k_scale or v_scale so far is no such power of two
  * raises the device error flag; its head's codes and scales are left as they were.
  * Each page written belongs to one sequence of the batch; a sequence with

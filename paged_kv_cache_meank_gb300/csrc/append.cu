@@ -95,14 +95,17 @@ append_kernel(AppendArgs a, int spans) {
     TP *dst = (is_k ? static_cast<TP *>(a.k_pages) : static_cast<TP *>(a.v_pages)) + head;
     TP *raw = is_k && a.raw_pages ? static_cast<TP *>(a.raw_pages) + head : nullptr;
 
-    float inv = 1.f;
+    float inv = 1.f, most = 448.f;                      // most: what an infinite entry counts as
+    bool odd = false;                                   // this lane has infinities or NaN
     if constexpr (SCALED) {
         const size_t so = ((size_t)srow * a.b.L + a.b.layer) * a.b.G + g;
         float *sp = (is_k ? a.k_scale : a.v_scale) + so;
         // read by all before one writes; K's and V's, as the block is left as it was where
         // either is no scale
         const float old_k = r0 > 0 ? a.k_scale[so] : 1.f, old_v = r0 > 0 ? a.v_scale[so] : 1.f;
-        float amax = 0.f;
+        // magnitudes compare as integers, infinities and NaN above all others: only where
+        // this lane has one of them are they told apart
+        uint32_t top_bits = 0;
 #pragma unroll
         for (int i = 0; i < ITERS; ++i) {
             if (on >> i & 1) {
@@ -110,10 +113,26 @@ append_kernel(AppendArgs a, int spans) {
                 VI::unpack(vx[i], x);
                 VI::unpack(vy[i], y);
 #pragma unroll
-                for (int k = 0; k < N; ++k) {
-                    const float ax = fabsf(x[k]), ay = fabsf(y[k]);
-                    if (ax < INFINITY) amax = fmaxf(amax, ax);   // NaN compares false
-                    if (ay < INFINITY) amax = fmaxf(amax, ay);
+                for (int k = 0; k < N; ++k)
+                    top_bits = max(top_bits, max(__float_as_uint(x[k]) & 0x7FFFFFFFu,
+                                                 __float_as_uint(y[k]) & 0x7FFFFFFFu));
+            }
+        }
+        odd = top_bits >= 0x7F800000u;
+        float amax = odd ? 0.f : __uint_as_float(top_bits);
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < ITERS; ++i) {
+                if (on >> i & 1) {
+                    float x[N], y[N];
+                    VI::unpack(vx[i], x);
+                    VI::unpack(vy[i], y);
+#pragma unroll
+                    for (int k = 0; k < N; ++k) {
+                        const float ax = fabsf(x[k]), ay = fabsf(y[k]);
+                        if (ax < INFINITY) amax = fmaxf(amax, ax);   // NaN compares false
+                        if (ay < INFINITY) amax = fmaxf(amax, ay);
+                    }
                 }
             }
         }
@@ -153,6 +172,7 @@ append_kernel(AppendArgs a, int spans) {
         }
         if (part == 0 && lane == 0) *sp = scale;
         inv = 1.f / scale;                              // exact: a power of two
+        most = 448.f * scale;
     }
 
 #pragma unroll
@@ -164,6 +184,14 @@ append_kernel(AppendArgs a, int spans) {
         VI::unpack(vy[i], y);
         TP *row = dst + (size_t)(r0 + j) * D + c * N;
         if (is_k) {
+            // infinity times a sine of 0, or infinity less infinity, would be NaN
+            if (SCALED && odd) {
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    if (fabsf(x[k]) == INFINITY) x[k] = copysignf(most, x[k]);
+                    if (fabsf(y[k]) == INFINITY) y[k] = copysignf(most, y[k]);
+                }
+            }
             const int64_t pos = a.positions ? (int64_t)a.positions[tok0 + j] : (int64_t)(lo + j);
             const float4 *t = reinterpret_cast<const float4 *>(a.table + pos * HD + c * N);
 #pragma unroll

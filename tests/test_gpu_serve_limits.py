@@ -257,3 +257,48 @@ def test_append_behind_a_stored_scale_that_is_none(kvm, side, bad):
         assert torch.equal(bits(got)[at], bits(was)[at]), "the block and head of the bad scale"
         good[at] = got[at]
         assert torch.equal(bits(got), bits(good)), "everything else"
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_entries_that_are_not_finite(kvm, act, d):
+    """Scaled pages: an infinity counts as 448 times the scale, which the finite entries
+    set, before K is rotated; a NaN stays one, and in K's rotated row its partner."""
+    G, n = 2, 40
+    ctx = context(kvm, L=1, G=G, H=4, d=d, kv="e4m3", act=act)
+    g = torch.Generator().manual_seed(9)
+    k, v = ((torch.randn(n, G, d, generator=g) * 3).to(TDT[act]) for _ in range(2))
+    h = d // 2
+    inf, nan = math.inf, math.nan
+    k[0, 0, 3], k[0, 0, 5 + h] = inf, -inf               # position 0: the sine is 0
+    k[1, 0, 3], k[1, 0, 3 + h] = inf, inf                # both of a pair
+    k[7, 1, 9], k[7, 1, 9 + h] = -inf, inf
+    k[33, 0, 1], k[34, 1, 2] = nan, inf
+    k[35, 0, 4], k[35, 0, 4 + h] = nan, inf
+    k[36] = inf                                          # a whole row
+    v[0, 0, 3], v[2, 1, 5], v[33, 0, 1] = inf, -inf, nan
+    kp, vp, raw = (torch.zeros(2, 1, G, 32, d, dtype=torch.uint8, device="cuda") for _ in range(3))
+    ks, vs = (torch.ones(2, 1, G, device="cuda") for _ in range(2))
+    cache = ctx.cache(kp, vp, ks, vs)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")     # noqa: E731
+    batch = ctx.batch(i32([0, n]), i32([n]), i32([[1, 0]]), n_tokens=n, max_q_len=n, max_kv_len=64)
+    ctx.append_kv(batch, cache, 0, k.cuda(), v.cuda(), raw_k_pages=raw)
+    ctx.sync()
+    for b, page in ((0, 1), (1, 0)):
+        rows = slice(32 * b, min(n, 32 * b + 32))
+        for gg in range(G):
+            for x, sc, pages, most, rot in ((k, ks, kp, 316.75, True), (k, ks, raw, 316.75, False),
+                                            (v, vs, vp, 448.0, False)):
+                x = x[rows, gg].double()
+                s = ref.scale_for(float(x[torch.isfinite(x)].abs().max()), most)
+                assert float(sc[page, 0, gg]) == s
+                x = torch.where(x.isinf(), torch.sign(x) * 448 * s, x) / s
+                mag = ref.pair_mag(x)
+                want = ref.rotate(x, torch.arange(n)[rows], 1e4) if rot else x
+                got = ref.decode(pages[page, 0, gg])[:want.shape[0]]
+                assert torch.equal(got.isnan(), want.isnan())
+                at = ~want.isnan()
+                sat = want.clamp(-448, 448)
+                # half an e4m3 step; the rotation's two products, sum, cos and sin, each rounded once
+                tol = (2.0 ** -4 * sat.abs()).clamp(min=2.0 ** -10) + (8 * U * mag if rot else 0)
+                assert ((got - sat).abs() <= tol)[at].all()
