@@ -617,17 +617,22 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
         const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
         uint32_t sn = 0, on = 0, on1 = 0, met = 0, met1 = 0, qn = 0, tiles = 0;   // phases met, tiles passed
+        // Tensor memory is read and written by whole warps, so they give up together: at
+        // once after wait(), at the end of the tile after the waits that every tile passes
+        // (a vote at each of those cost 32 tokens over 65568 e4m3 keys 3 us).
         bool ok = true;
+        auto wait = [&](uint64_t *b, uint32_t parity) {
+            return ok = __all_sync(0xffffffffu, tc::mbar_wait(b, parity, kWaitNs));
+        };
         auto meet = [&](int which, uint32_t parity) {    // both groups
             tc::mbar_arrive(&bar->meet[which]);
-            ok = tc::mbar_wait(&bar->meet[which], parity, kWaitNs);
-            return ok;
+            return wait(&bar->meet[which], parity);
         };
         Seg shared[2];                                   // the tiles shared with other CTAs
         int n_shared = 0;
         for (int sg = 0; ok; ++sg) {
             const Seg *seg = open(sg);
-            if (seg == nullptr) {
+            if (!__all_sync(0xffffffffu, seg != nullptr)) {
                 ok = false;
                 break;
             }
@@ -703,10 +708,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     tc::fence_proxy_async_smem();
                     tc::mbar_arrive(&bar->q_full[PAIR ? gr : 0]);
                     if constexpr (E4) {                  // the power of two of this thread's row
-                        if (!tc::mbar_wait(&bar->q_full[PAIR ? gr : 0], qn & 1, kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!wait(&bar->q_full[PAIR ? gr : 0], qn & 1)) break;
                         c *= qpow[(PAIR ? gr * TR : 0) + row];
                     }
                     ++qn;
@@ -726,10 +728,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const bool head = j < step;              // the group's first tile of the segment
                 if constexpr (E4) {
                     const uint32_t tile = tiles + j;
-                    if (!tc::mbar_wait(&bar->sc_full[tile % kScales], (tile / kScales) & 1, kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!tc::mbar_wait(&bar->sc_full[tile % kScales], (tile / kScales) & 1, kWaitNs)) ok = false;
                 }
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -742,10 +741,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             lv[i] = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
                         }
                     }
-                    if (!tc::mbar_wait(&bar->s_full[gr][h], sn & 1, kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!tc::mbar_wait(&bar->s_full[gr][h], sn & 1, kWaitNs)) ok = false;
                     tc::tc_fence_after();
                     uint32_t s[HK];
                     const uint32_t sc = ts + (h == 0 ? a_col : a_col ^ HK);
@@ -854,27 +850,24 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     }
                     l += sum;
                     if (!head && !(early >> h & 1) &&
-                        !tc::mbar_wait(&bar->pv_done[gr][h], (sn - 1) & 1, kWaitNs)) {
+                        !tc::mbar_wait(&bar->pv_done[gr][h], (sn - 1) & 1, kWaitNs))
                         ok = false;
-                        break;
-                    }
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     tc::mbar_arrive(&bar->p_full[gr][h]);
                 }
                 early >>= 2;
+                ok = __all_sync(0xffffffffu, ok);
             }
             if (!ok) break;
             tiles += T;
             // ------------------------------------------------ the segment's end
             const bool mine = T > (PAIR ? 0 : gr);      // this group has an O
             if (mine) {
-                if (!tc::mbar_wait(&bar->o_full[gr], on & 1, kWaitNs) ||
-                    !(early & 1 || tc::mbar_wait(&bar->pv_done[gr][0], (sn - 1) & 1, kWaitNs)) ||
-                    !tc::mbar_wait(&bar->pv_done[gr][1], (sn - 1) & 1, kWaitNs)) {
-                    ok = false;
+                if (!wait(&bar->o_full[gr], on & 1) ||
+                    !(early & 1 || wait(&bar->pv_done[gr][0], (sn - 1) & 1)) ||
+                    !wait(&bar->pv_done[gr][1], (sn - 1) & 1))
                     break;
-                }
                 ++on;
             }
             // O to units of 2^m
@@ -888,10 +881,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (gr == 0) {                          // group 0 writes the rows
                     const float2 o1 = ml1[row];
                     if (T > 1) {
-                        if (!tc::mbar_wait(&bar->o_full[1], on1 & 1, kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!wait(&bar->o_full[1], on1 & 1)) break;
                         ++on1;
                     }
                     const float mm = fmaxf(m, o1.x), base = mm == -INFINITY ? 0.f : mm;
