@@ -647,7 +647,10 @@ kvm_status kvm_host_free(void *ptr);
  * kvm_step; passes 1 and 2 both count) runs with its TMA producer idle, so
  * its bounded device waits run out after about a second each; the call
  * itself returns KVM_OK and the next kvm_sync returns KVM_ERR_TIMEOUT.  Its
- * scores and selection are then meaningless (ids stay in range).  what = 0
+ * scores and selection are then meaningless (ids stay in range).  what = 4:
+ * the n-th next kvm_attend, where it runs in tiles on the tensor cores (more than
+ * 16 query rows of a kv head, bf16 queries, bf16 or e4m3 pages), fetches only the
+ * first 128 keys of one of its CTAs, with the same outcome.  what = 0
  * clears.  The context stays usable in every case. */
 kvm_status kvm_debug_inject(kvm_ctx *ctx, int32_t what, int64_t nth);
 

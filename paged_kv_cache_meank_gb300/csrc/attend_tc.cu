@@ -45,7 +45,8 @@
 // shared-memory traffic, about 4150 clocks: 32 tokens over 65568 keys 77 us.  Small
 // calls are bound by their start (9 thousand clocks to the first scores) and joins.
 // Every wait is bounded to a second; on timeout the device error flag (bit 4) is
-// raised and the CTA winds down as the scoring kernels do.
+// raised and the CTA winds down: copies and products under way end before shared and
+// tensor memory do.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <math.h>
@@ -113,7 +114,7 @@ constexpr int kScales = 4;      // tiles whose pages' scales are kept (see the c
 
 struct Bars {
     uint64_t full[8], empty[8], raw_full[8], raw_empty[8], s_full[2][2], p_full[2][2], pv_done[2][2], sb_free[2], o_full[2], q_full[2];
-    uint64_t seg_full[kSegs], seg_empty[kSegs], meet[2], v_clear[8], sc_full[kScales];
+    uint64_t seg_full[kSegs], seg_empty[kSegs], meet[2], v_clear[8], sc_full[kScales], drained[2];
     Seg seg[kSegs];
     float2 scale[kScales][kPagesPerTile];   // e4m3: (k_scale, v_scale) of a tile's pages
     uint32_t tmem;
@@ -335,6 +336,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             tc::mbar_init(&bar->o_full[s], 1);
             tc::mbar_init(&bar->q_full[s], PAIR ? 128 : 256);
             tc::mbar_init(&bar->meet[s], 256);
+            tc::mbar_init(&bar->drained[s], 1);
         }
         for (int s = 0; s < kScales; ++s) tc::mbar_init(&bar->sc_full[s], kPagesPerTile);
         for (int s = 0; s < kSegs; ++s) {
@@ -382,10 +384,12 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     ok = false;
                     break;
                 }
-                const int T = seg->T, u0 = seg->u0, kv_len = seg->kv, g = seg->g;
+                int T = seg->T;
+                const int u0 = seg->u0, kv_len = seg->kv, g = seg->g;
                 const int32_t *table = a.b.page_table + (int64_t)seg->s * a.b.table_stride;
                 close(sg);
                 if (T < 0) break;
+                if (a.stall && blockIdx.x == 0) T = n == 0;   // fault injection: the first key tile alone
                 const int n_pages = (kv_len + kBlockTokens - 1) / kBlockTokens;
                 int32_t ids = -1;
                 for (int j = 0; j < T && ok; ++j) {
@@ -451,7 +455,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             uint64_t *q_full = &bar->q_full[PAIR ? gr : 0];
             constexpr int step = PAIR ? 1 : 2;
             int n = 0;                                   // K / V tiles of earlier segments
-            uint32_t qn = 0, pn = 0, on = 0;             // uses of q_full, p_full, o_full
+            uint32_t qn = 0, pn = 0;                     // uses of q_full, p_full
             uint32_t cleared = 0;                        // parity of each slot's v_clear
             bool ok = true;
             // a warp-wide wait: false once one has given up
@@ -558,15 +562,16 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         pv(j, 1, a_col + HK / 2);
                         if (next) qk(j + step, 1, a_col);
                         ++pn;
-                        if (!next) ++on;
                     }
                 }
                 n += 2 * T;
             }
+            // every product issued is done before tensor memory is freed, those of a segment
+            // given up part-way too
+            if (tc::elect_one()) tc::mma_commit(&bar->drained[gr]);
+            __syncwarp();
+            if (!tc::mbar_wait(&bar->drained[gr], 0, kWaitNs)) ok = false;
             if (!ok && lane == 0) atomicOr(err, 4);
-            // the last commit covers every MMA issued: done before TMEM is freed
-            if (on > 0 && !tc::mbar_wait(&bar->o_full[gr], (on - 1) & 1, kWaitNs))
-                if (lane == 0) atomicOr(err, 4);
         } else if (warp == 2) {
             // ---------------------------------------------------- the walk
             using W = Walk<RB, TK>;
@@ -1001,7 +1006,12 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
             }
         }
-        if (!ok) atomicOr(err, 4);
+        if (!ok) {
+            // what is under way lands before the CTA ends
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            tc::tmem_wait_st();
+            atomicOr(err, 4);
+        }
     } else {
         // -------------------------------------------------------- e4m3 -> f16
         if constexpr (E4) {

@@ -363,6 +363,8 @@ kvm::CtxView kvm::ctx_view(const kvm_ctx *c) {
     return v;
 }
 
+bool kvm::take_injection(kvm_ctx *c, int what) { return injected(c, what); }
+
 extern "C" {
 
 size_t kvm_workspace_bytes(const kvm_config *cfg) {
@@ -1247,8 +1249,8 @@ kvm_status kvm_host_free(void *ptr) {
 
 kvm_status kvm_debug_inject(kvm_ctx *c, int32_t what, int64_t nth) {
     if (!c) return fail(KVM_ERR_INVALID_ARG, "ctx is NULL");
-    if (what < 0 || what > 3 || (what != 0 && nth < 1))
-        return fail(KVM_ERR_INVALID_ARG, "what must be 0..3 and nth >= 1");
+    if (what < 0 || what > 4 || (what != 0 && nth < 1))
+        return fail(KVM_ERR_INVALID_ARG, "what must be 0..4 and nth >= 1");
     c->inject_what = what;
     c->inject_nth = nth;
     c->inject_seen = 0;

@@ -36,6 +36,8 @@ struct CtxView {
     int device;
 };
 CtxView ctx_view(const kvm_ctx *c);
+// Whether an injected failure of this kind (kvm_debug_inject) is due now.
+bool take_injection(kvm_ctx *c, int what);
 
 constexpr int kBlockTokens = 32;
 constexpr int kMaxHalfDim = 64;       // head_dim <= 128
@@ -270,6 +272,7 @@ struct AttendArgs {
     float *lse;
     float *part;                   // partial outputs (attend_scratch_bytes)
     int *count;                    // arrivals, departures: [2][kAttendMaxCtas], zero between calls
+    int stall;                     // fault injection: CTA 0 of the tile form fetches one key tile only
 };
 constexpr int kAttendMaxCtas = 608;    // CTAs of one attention grid, at most
 size_t attend_scratch_bytes();         // of AttendArgs::part

@@ -295,6 +295,7 @@ kvm_status kvm_attend(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *cac
     a.lse = lse;
     a.part = c.attend_part;
     a.count = c.attend_count;
+    a.stall = kvm::take_injection(ctx, 4) ? 1 : 0;
     bool too_large = false;
     const cudaError_t e = kvm::launch_attend(c.q_dtype, c.kv_dtype, a,
                                              reinterpret_cast<cudaStream_t>(stream), &too_large);

@@ -10,7 +10,7 @@ import torch
 
 import serve_ref as ref
 from serve_ref import EPS2, TDT, U, Paged
-from test_gpu_serve import context, kvm   # noqa: F401
+from test_gpu_serve import context, kvm, run_attend   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -302,3 +302,39 @@ def test_append_entries_that_are_not_finite(kvm, act, d):
                 # half an e4m3 step; the rotation's two products, sum, cos and sin, each rounded once
                 tol = (2.0 ** -4 * sat.abs()).clamp(min=2.0 ** -10) + (8 * U * mag if rot else 0)
                 assert ((got - sat).abs() <= tol)[at].all()
+
+
+# ---------------------------------------------------------------- waits that give up
+
+@pytest.mark.parametrize("kv,scaled", [("bf16", False), ("e4m3", True)])
+@pytest.mark.parametrize("G,lens", [(1, [(40, 9000)]), (2, [(300, 4000), (9, 700)]), (4, [(600, 3000)])],
+                         ids=["single row tiles", "cut and ragged", "pairs"])
+def test_attend_bounded_waits_and_recovery(kvm, kv, scaled, G, lens):
+    """One CTA's producer stops after its first key tile: waits run out, the parts of
+    shared tiles stay uncounted, kvm_sync reports KVM_ERR_TIMEOUT, and the next
+    calls of every form on the same context are right."""
+    import time
+    ctx = kvm.Context(kvm.config_for(ref.workload(G=G, H=6 * G, d=64, kv=kv, act="bf16")))
+    p = Paged(lens, G=G, H=6 * G, d=64, kv=kv, act="bf16", scaled=scaled, seed=10)
+    batch, cache = p.on(ctx)
+    out = torch.zeros(p.n, p.H, 64, device="cuda", dtype=torch.bfloat16)
+    q = p.q.cuda()
+    ctx.attend(batch, cache, 0, q, out)
+    ctx.sync()
+    want = out.clone()
+    ctx.debug_inject(4, 2)
+    ctx.attend(batch, cache, 0, q, out)                  # the first is as ever
+    ctx.sync()
+    assert torch.equal(out, want)
+    t0 = time.monotonic()
+    ctx.attend(batch, cache, 0, q, out)
+    with pytest.raises(kvm.KvmError) as e:
+        ctx.sync()
+    assert e.value.name == "KVM_ERR_TIMEOUT"
+    assert time.monotonic() - t0 < 30.0
+    for again in (p, Paged([(1, 3000), (1, 1000)], G=G, H=6 * G, d=64, kv=kv, act="bf16", scaled=scaled, seed=11), p):
+        run_attend(kvm, again, True, ctx=ctx)
+    ctx.attend(batch, cache, 0, q, out)
+    ctx.sync()
+    assert torch.equal(out, want)
+    ctx.close()
