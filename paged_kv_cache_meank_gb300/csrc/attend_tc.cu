@@ -75,6 +75,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLeast = 1e-37f;            // of a score's factor: 0 * -inf is no mask
 constexpr float kLn2 = 0.6931471805599453f;
 
+constexpr int kScales = 4;      // tiles whose pages' scales are kept (see Lay)
+
 template <int D, bool E4, bool PAIR>
 struct Lay {
     static constexpr int KA = D / 64;                  // 128-byte atoms of a row
@@ -96,6 +98,10 @@ struct Lay {
     static constexpr int SMEM = OFF_BAR + 1024;
     static constexpr int THREADS = E4 ? 512 : 384;
     static_assert(SLOTS * TILE >= kPreInts * 4, "prefix fits the ring");
+    // The converter writes the scales of tile t over those of tile t - kScales.  It has
+    // filled V of tile t - 1 before, use 2t - 1 of the ring, so every use up to 2t - 1 - SLOTS
+    // has been consumed; V of tile t - kScales, use 2 (t - kScales) + 1, is one of them.
+    static_assert(!E4 || SLOTS <= 2 * kScales - 2, "a tile's scales are read before they are replaced");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -110,7 +116,6 @@ struct Seg {
 };
 
 constexpr int kSegs = 4;        // segments handed out ahead
-constexpr int kScales = 4;      // tiles whose pages' scales are kept (see the converter)
 
 struct Bars {
     uint64_t full[8], empty[8], raw_full[8], raw_empty[8], s_full[2][2], p_full[2][2], pv_done[2][2], sb_free[2], o_full[2], q_full[2];
@@ -1065,8 +1070,7 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             break;
                         }
                         if (kv == 0 && lane == 0) {
-                            // K's slot was V's of the tile before the last, which both groups
-                            // are done with: the place of four tiles ago is free
+                            // the place of tile t - kScales is free (see Lay)
                             const int x = (n >> 1) % kScales;
                             bar->scale[x][w] = sc;
                             tc::mbar_arrive(&bar->sc_full[x]);
