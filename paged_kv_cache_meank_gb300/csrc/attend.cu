@@ -35,7 +35,11 @@ struct Lay {
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = RB * D;
     static constexpr int FLOATS = OFF_P + NBUF * PAGE;
-    static constexpr int SMEM = FLOATS * 4 + kPreInts * 4;
+    static constexpr int SMEM = FLOATS * 4 + kPlainPreInts * 4;
+    // CTAs of an SM: equal runs need all of the grid at once.  (The SM has 228 KB, a CTA's
+    // own 1 KB and its static variables among them.)
+    static constexpr int PER_SM = KS ? (D == 128 ? 1 : 3) : 4;
+    static_assert(PER_SM * (SMEM + 1024 + 64) <= 228 * 1024, "the grid runs at once");
 };
 
 }  // namespace
@@ -311,8 +315,7 @@ static cudaError_t simt_t(const AttendArgs &a, cudaStream_t s) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int per_sm = KS ? (D == 128 ? 1 : 3) : 4;
-    const int ctas = min(kAttendMaxCtas, sm_count() * per_sm);
+    const int ctas = min(kAttendMaxCtas, sm_count() * Lay<D, KS>::PER_SM);
     kern<<<ctas, kWarps * 32, smem, s>>>(a, KS ? 8 : 4);
     note_launch();
     return cudaGetLastError();

@@ -66,8 +66,8 @@ struct Line {
         return max(1, (keys(i, a, r) + UNIT - 1) / UNIT);
     }
     // Lays the line out: pre[s] = units of the sequences before s, or with `pad`
-    // their row tiles (pre: kPreInts in shared memory).  By one warp, a lane to a
-    // sequence.
+    // their row tiles (pre: kPreInts in shared memory, without PAD kPlainPreInts).  By one
+    // warp, a lane to a sequence.
     template <bool PAD>
     __device__ static LineInfo lay_out(const AttendArgs &a, int *pre, int n_ctas, int min_units, int join) {
         const int lane = threadIdx.x & 31;
@@ -111,7 +111,10 @@ struct Line {
             li.total += __shfl_sync(0xffffffffu, w, last);
             items += __shfl_sync(0xffffffffu, n, last);
         }
-        if (lane == 0) pre[0] = pre[kMaxSeqs + 1] = 0;
+        if (lane == 0) {
+            pre[0] = 0;
+            if (PAD) pre[kMaxSeqs + 1] = 0;
+        }
         li.most = __reduce_max_sync(0xffffffffu, li.most);
         plan<PAD>(li, items, n_ctas, min_units, join);
         __syncwarp();
@@ -170,7 +173,7 @@ struct Line {
     }
 };
 
-constexpr int kPreInts = 2 * (kMaxSeqs + 1);   // shared memory of lay_out
+constexpr int kPreInts = 2 * (kMaxSeqs + 1), kPlainPreInts = kMaxSeqs + 1;   // shared memory of lay_out
 
 // A walk over one CTA's run of the line.
 template <int RB, int UNIT>
