@@ -29,6 +29,7 @@ __device__ inline const T *typed(const void *p) { return static_cast<const T *>(
 template <int D, bool KS>
 struct Lay {
     static constexpr int RB = KS ? kRows : kRows * kWarps;
+    static_assert(RB <= kSimtMaxRows, "parts are for so many");
     static constexpr int KST = D + 4;      // padded K row: lanes' 16-byte reads hit distinct banks
     static constexpr int PAGE = kBlockTokens * (KST + D);
     static constexpr int NBUF = KS ? kWarps : 1;
@@ -335,7 +336,10 @@ static cudaError_t simt_q(int kv_dtype, const AttendArgs &a, cudaStream_t s) {
     return simt_d<TQ, e4m3>(a, s);
 }
 
-size_t attend_scratch_bytes() { return kAttendPartFloats * sizeof(float); }
+size_t attend_scratch_bytes(int q_dtype, int kv_dtype, int d) {
+    const bool tensor_cores = q_dtype == BF16 && kv_dtype != F32;
+    return (tensor_cores ? max(kTilePartRows, kSimtPartRows) : kSimtPartRows) * (d + 2) * sizeof(float);
+}
 
 cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s,
                           bool *too_large) {

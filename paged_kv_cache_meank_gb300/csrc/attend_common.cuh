@@ -272,9 +272,11 @@ __host__ __device__ __forceinline__ size_t part_slot(int cta, bool first) {
     return (size_t)cta * 2 + (first ? 1 : 0);
 }
 
-// CTAs and query rows of the largest records (the tensor-core tile kernel's).
-constexpr int kTileMaxCtas = 160, kTileMaxRows = 256;
-constexpr size_t kAttendPartFloats = (size_t)kTileMaxCtas * 2 * kTileMaxRows * 130;
+// Rows of partial results, d + 2 floats each: two places a CTA of each form.  The float32
+// form may take any call, the other two bf16 queries over bf16 or e4m3 pages.
+constexpr int kTileMaxCtas = 160, kTileMaxRows = 256, kSimtMaxRows = 16;
+constexpr size_t kTilePartRows = (size_t)kTileMaxCtas * 2 * kTileMaxRows;
+constexpr size_t kSimtPartRows = (size_t)kAttendMaxCtas * 2 * kSimtMaxRows;
 
 // attend_decode.cu: up to kDecodeRows query rows of a kv head, the same types.
 constexpr int kDecodeRows = 16;

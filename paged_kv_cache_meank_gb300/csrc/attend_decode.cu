@@ -65,7 +65,8 @@ struct Lay {
     static constexpr int BYTES = W * (RING > REC * 4 ? RING : REC * 4);
     static constexpr int MAX_CTAS = CTAS * kTileMaxCtas;
     static constexpr int WEIGHTS = MAX_CTAS * RB * 4;      // bytes: of the parts of a join
-    static_assert(MAX_CTAS <= kAttendMaxCtas, "counts and parts are for so many");
+    static_assert(MAX_CTAS <= kAttendMaxCtas, "counts are for so many");
+    static_assert((size_t)MAX_CTAS * 2 * RB <= kTilePartRows, "parts are for so many");
     static constexpr int SMEM = BYTES + kPreInts * 4;
 };
 

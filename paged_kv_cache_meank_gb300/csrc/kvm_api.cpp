@@ -158,7 +158,7 @@ Layout layout_of(const kvm_config *c) {
     lo.resid = take(((size_t)2 * c->max_blocks + (size_t)4 * c->pool_pages + c->view_blocks +
                      (size_t)(kStatSlots + 1) * 8 + 1) *
                     sizeof(int32_t));
-    lo.attend = take(kvm::attend_scratch_bytes());
+    lo.attend = take(kvm::attend_scratch_bytes(c->q_dtype, c->kv_dtype, c->head_dim));
     lo.attend_count = take(2 * kvm::kAttendMaxCtas * sizeof(int));
     lo.err = take(256);
     lo.total = off;

@@ -275,7 +275,7 @@ struct AttendArgs {
     int stall;                     // fault injection: CTA 0 of the tile form fetches one key tile only
 };
 constexpr int kAttendMaxCtas = 608;    // CTAs of one attention grid, at most
-size_t attend_scratch_bytes();         // of AttendArgs::part
+size_t attend_scratch_bytes(int q_dtype, int kv_dtype, int d);   // of AttendArgs::part
 // Sets *too_large instead of launching where the call's bounds are beyond 32 bits.
 cudaError_t launch_attend(int q_dtype, int kv_dtype, const AttendArgs &a, cudaStream_t s,
                           bool *too_large);
