@@ -165,6 +165,7 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
     if (!ctx) return fail(KVM_ERR_INVALID_ARG, "ctx is NULL");
     const kvm::CtxView c = kvm::ctx_view(ctx);
     if (n_tokens < 0) return fail(KVM_ERR_INVALID_ARG, "n_tokens < 0");
+    if (n_tokens == 0) return KVM_OK;   // (buffers of no tokens may have no address)
     if (!q && !k) return fail(KVM_ERR_INVALID_ARG, "q or k is required");
     if ((q != nullptr) != (q_free || q_rot) || (k != nullptr) != (k_free || k_rot))
         return fail(KVM_ERR_INVALID_ARG, "each given side needs an output, and only it");
@@ -175,7 +176,6 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(KVM_ERR_INVALID_ARG, "eps must be >= 0");
     if (q) KVM_TRY(row_stride(q_stride, c.H, c.d, c.q_dtype, "q"));
     if (k) KVM_TRY(row_stride(k_stride, c.G, c.d, c.q_dtype, "k"));
-    if (n_tokens == 0) return KVM_OK;
     if (!positions) return fail(KVM_ERR_INVALID_ARG, "positions are required");
     // an output that is its own input has to have the input's rows
     if ((q && (q == q_free || q == q_rot) && q_stride != (int64_t)c.H * c.d) ||

@@ -338,3 +338,15 @@ def test_attend_bounded_waits_and_recovery(kvm, kv, scaled, G, lens):
     ctx.sync()
     assert torch.equal(out, want)
     ctx.close()
+
+
+# ---------------------------------------------------------------- the binding
+
+def test_calls_of_no_tokens(kvm):
+    """Empty tensors (whose address is none) do nothing."""
+    ctx = context(kvm, L=1, G=2, H=4, d=64, kv="bf16", act="bf16")
+    z = lambda h: torch.empty(0, h, 64, device="cuda", dtype=torch.bfloat16)     # noqa: E731
+    n0 = kvm.launch_count()
+    ctx.qk_norm_rope(torch.empty(0, dtype=torch.int32, device="cuda"), q=z(4), k=z(2), q_rot=z(4), q_free=z(4),
+                     k_free=z(2), q_weight=torch.ones(64, device="cuda").bfloat16())
+    assert kvm.launch_count() == n0
