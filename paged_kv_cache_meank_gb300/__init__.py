@@ -323,7 +323,7 @@ class Context:
         if not (t.dtype is dt and len(shape) == 3 and shape[0] >= n and shape[1] == heads
                 and shape[2] == d and stride[2] == 1 and (stride[1] == d or heads == 1)):
             raise ValueError(f"{name}: {dt} [>= {n}][{heads}][{d}], heads packed")
-        return stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+        return stride[0] if shape[0] > 1 else heads * d   # (that of a single row means nothing)
 
     def _packed(self, name, t, heads: int, n: int) -> int | None:
         """Checks a contiguous output [n][heads][d] of q_dtype; its address."""

@@ -350,3 +350,24 @@ def test_calls_of_no_tokens(kvm):
     ctx.qk_norm_rope(torch.empty(0, dtype=torch.int32, device="cuda"), q=z(4), k=z(2), q_rot=z(4), q_free=z(4),
                      k_free=z(2), q_weight=torch.ones(64, device="cuda").bfloat16())
     assert kvm.launch_count() == n0
+
+
+def test_one_token_of_any_row_stride(kvm):
+    """The stride of a dimension of one element means nothing."""
+    ctx = context(kvm, L=1, G=1, H=4, d=64, kv="bf16", act="bf16")
+    p = Paged([(1, 40)], G=1, H=4, d=64, kv="bf16", act="bf16", seed=12)
+    batch, cache = p.on(ctx)
+    pos = torch.tensor([39], dtype=torch.int32, device="cuda")
+    base = torch.randn(4, 64, device="cuda").bfloat16()
+    got = []
+    for stride in (256, 259):
+        q = torch.as_strided(base, (1, 4, 64), (stride, 64, 1))
+        k = torch.as_strided(base, (1, 1, 64), (stride - 192, stride - 192, 1))
+        out, rot = (torch.zeros(1, 4, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        ctx.append_kv(batch, cache, 0, k, k)
+        ctx.qk_norm_rope(pos, q=q, q_rot=rot)
+        ctx.attend(batch, cache, 0, q, out)
+        ctx.sync()
+        got.append((p.dk.clone(), rot, out))
+    for a, b in zip(*got):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
