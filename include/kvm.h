@@ -556,7 +556,8 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * Bases and strides multiples of 16 bytes; all buffers device memory.
  * softmax_scale is usually 1 / sqrt(d); at most 1e30 in magnitude.
  * bf16 queries over bf16 or e4m3 pages run on the tensor cores: products and
- * sums in float32, with the weights rounded to bf16 before the product with V;
+ * sums in float32, with the weights rounded to bf16 before the product with V
+ * (up to 16 query rows of a kv head: to the sum of two bf16, 2^-17 of them);
  * over e4m3 pages each weight times its v_scale is rounded to float16 against the
  * largest such product of its row (below 2^-21 of it the rounding is absolute,
  * 2^-32 of it at most), and query entries below 2^-32 of their row's largest are

@@ -14,7 +14,9 @@
 // (these products are far from what bounds the kernel, and their operands come
 // out of registers: tensor memory would only add round trips).  As in
 // attend_tc.cu the maximum moves when a stage exceeds it by 2^8; a vote decides,
-// so the usual stage has no shuffles.
+// so the usual stage has no shuffles.  A weight goes into the product with V as the
+// sum of two bf16 (its rounding, and that of the rest), with two products: the matrix
+// pipe is far from busy, and 32768 keys take the same time with one.
 //
 // e4m3: as in attend_tc.cu codes become f16 (exact) in registers, q is divided by
 // a power of two per row, the page's k_scale goes into the factor of the scores
@@ -404,7 +406,9 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                     }
             }
             // ---- weights, and the product with V
-            uint32_t pf[KEYS / 16][NT][2];
+            // bf16 pages: a weight as the sum of two bf16
+            constexpr int PARTS = E4 ? 1 : 2;
+            uint32_t pf[PARTS][KEYS / 16][NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float base[2], w[2];
@@ -422,8 +426,15 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                         l[t][e & 1] += p[e];
                         if (E4) p[e] *= w[e & 1];
                     }
-                    pf[u][t][0] = transposed(pack<E4>(p[0], p[1]));
-                    pf[u][t][1] = transposed(pack<E4>(p[2], p[3]));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t two = pack<E4>(p[2 * h], p[2 * h + 1]);
+                        pf[0][u][t][h] = transposed(two);
+                        if constexpr (!E4)
+                            pf[1][u][t][h] = transposed(
+                                pack<false>(p[2 * h] - __uint_as_float(two << 16),
+                                            p[2 * h + 1] - __uint_as_float(two & 0xFFFF0000u)));
+                    }
                 }
             }
 #pragma unroll
@@ -435,7 +446,10 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                         uint32_t f[4];
                         ldm4t(f, vb + place(row, 2 * i + ((lane >> 3) & 1)));
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) mma<false>(o[i][t], f, pf[u][t][0], pf[u][t][1]);
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int y = 0; y < PARTS; ++y)
+                                mma<false>(o[i][t], f, pf[y][u][t][0], pf[y][u][t][1]);
                     }
                 } else {
                     const int row = u * 16 + (lane & 15);
@@ -452,7 +466,7 @@ attend_decode_kernel(const __grid_constant__ AttendArgs a) {
                             e4m3_f16(__byte_perm(f[2 * y + 1], 0, 0x3120), fa[2], fa[3]);
 #pragma unroll
                             for (int t = 0; t < NT; ++t)
-                                mma<true>(o[i + y][t], fa, pf[u][t][0], pf[u][t][1]);
+                                mma<true>(o[i + y][t], fa, pf[0][u][t][0], pf[0][u][t][1]);
                         }
                     }
                 }

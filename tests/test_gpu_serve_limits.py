@@ -371,3 +371,22 @@ def test_one_token_of_any_row_stride(kvm):
         got.append((p.dk.clone(), rot, out))
     for a, b in zip(*got):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# ---------------------------------------------------------------- weights of decoded tokens
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q,kv_len", [(1, 3), (1, 40), (2, 5), (2, 300), (1, 3000)])
+def test_attend_decode_keeps_its_weights(kvm, q, kv_len, d):
+    """bf16 pages, up to 16 query rows: weights are held as the sum of two bf16, so
+    that what is left of values that cancel is not their rounding."""
+    p = Paged([(q, kv_len), (q, kv_len)], G=2, H=12, d=d, kv="bf16", act="bf16", seed=14, qstd=0.3)
+    p.v = (p.v.double().sign() * (100 + p.v.double().abs())).bfloat16()
+    out, _ = attend(kvm, p, d ** -0.5)
+    want, _, absv, ds = p.reference(d ** -0.5, True)
+    # the output's rounding; of the weights, the second bf16's rounding (2^-8 of 2^-8),
+    # and what float32 leaves, as in ref.attend_tolerance
+    w = 2 * ds[..., None] + (2 * kv_len + 16) * U + 2.0 ** -16
+    err = (out - want).abs()
+    tol = EPS2["bf16"] * want.abs() + w * (1 + EPS2["bf16"]) * absv
+    assert (err <= tol).all(), f"worst error / tolerance {(err / tol).max():.3g}"
