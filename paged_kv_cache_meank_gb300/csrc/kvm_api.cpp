@@ -1182,17 +1182,21 @@ kvm_status kvm_step(kvm_ctx *c, const void *q, int32_t n_queries, int64_t n_bloc
 
 kvm_status kvm_sync(kvm_ctx *c, kvm_stream stream) {
     if (!c) return fail(KVM_ERR_INVALID_ARG, "ctx is NULL");
-    KVM_CUDA(cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    KVM_CUDA(cudaStreamSynchronize(s));
     KVM_CUDA(cudaStreamSynchronize(c->copy_stream));
     if (kvm_status st = flush_pending(c); st != KVM_OK) return st;
     int flag = 0;
     KVM_CUDA(cudaMemcpy(&flag, c->err_dev, sizeof(int), cudaMemcpyDeviceToHost));
     if (flag) {
-        KVM_CUDA(cudaMemset(c->err_dev, 0, sizeof(int)));
+        // both are done when this returns: the next call's stream may be one that does not
+        // wait for the default stream
+        KVM_CUDA(cudaMemsetAsync(c->err_dev, 0, sizeof(int), s));
         // an attention call that gave up may have left its arrival counts
         if (flag & 4)
-            KVM_CUDA(cudaMemset(c->ws + c->lo.attend_count, 0,
-                                2 * kvm::kAttendMaxCtas * sizeof(int)));
+            KVM_CUDA(cudaMemsetAsync(c->ws + c->lo.attend_count, 0,
+                                     2 * kvm::kAttendMaxCtas * sizeof(int), s));
+        KVM_CUDA(cudaStreamSynchronize(s));
         if (flag & 4) return fail(KVM_ERR_TIMEOUT, "a bounded device wait gave up (flag 0x%x)", flag);
         return fail(KVM_ERR_DEVICE, "device range check raised flag 0x%x", flag);
     }

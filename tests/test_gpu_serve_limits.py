@@ -340,6 +340,30 @@ def test_attend_bounded_waits_and_recovery(kvm, kv, scaled, G, lens):
     ctx.close()
 
 
+def test_attend_recovers_on_a_stream_of_its_own(kvm):
+    """The counters are cleared when kvm_sync returns, for a stream that does not wait for
+    the default one."""
+    p = Paged([(600, 3000)], G=4, H=24, d=64, kv="bf16", act="bf16", seed=13)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        ctx = kvm.Context(kvm.config_for(ref.workload(G=4, H=24, d=64, kv="bf16", act="bf16")))
+        batch, cache = p.on(ctx)
+        q, out = p.q.cuda(), torch.zeros(p.n, 24, 64, device="cuda", dtype=torch.bfloat16)
+        ctx.attend(batch, cache, 0, q, out)
+        ctx.sync(s)
+        want = out.clone()
+        ctx.debug_inject(4, 1)
+        ctx.attend(batch, cache, 0, q, out)
+        with pytest.raises(kvm.KvmError) as e:
+            ctx.sync(s)
+        assert e.value.name == "KVM_ERR_TIMEOUT"
+        for _ in range(5):
+            ctx.attend(batch, cache, 0, q, out)
+        ctx.sync(s)
+        assert torch.equal(out, want)
+        ctx.close()
+
+
 # ---------------------------------------------------------------- the binding
 
 def test_calls_of_no_tokens(kvm):
