@@ -44,7 +44,7 @@
 // that let a half be weighed while the other is made), and is passed in about
 // 2760: 2048 query tokens over 34816 bf16 keys (1.7 TFLOP) in 1.18 ms, 1440
 // TFLOP/s, 0.75 of the measured burst rate.  e4m3 pages add conversions and their
-// shared-memory traffic, about 4150 clocks: 32 tokens over 65568 keys 77 us.  Small
+// shared-memory traffic, about 4050 clocks: 32 tokens over 65568 keys 74 us.  Small
 // calls are bound by their start (9 thousand clocks to the first scores) and joins.
 // Every wait is bounded to a second; on timeout the device error flag (bit 4) is
 // raised and the CTA winds down: copies and products under way end before shared and
@@ -106,6 +106,25 @@ struct Lay {
     static_assert(!E4 || SLOTS <= 2 * kScales - 2, "a tile's scales are read before they are replaced");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// A bounded wait (tc::mbar_wait) of a whole warp, whose lanes leave it together: every
+// branch goes by a vote.  Tensor memory is read and written by whole warps, so none may
+// give up alone.  (A wait of each lane on its own and a vote at the end of the tile took
+// 2048 tokens over 34816 e4m3 keys 1515 us against 1433, 32 over 65568 78 against 74.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t t0 = 0;
+    for (uint32_t n = 0; n < (1u << 30); ++n) {
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+        if ((n & 63) == 63) {
+            const uint32_t t = tc::global_ns_lo();
+            if (n == 63)
+                t0 = t;
+            else if (__any_sync(0xffffffffu, t - t0 > kWaitNs))
+                return false;
+        }
+    }
+    return false;
+}
 
 // One segment of the CTA's run, as the roles need it.
 struct Seg {
@@ -629,22 +648,23 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
         const uint32_t keep = a.scale == 0.f ? 0u : 0xFFFFFFFFu;
         uint32_t sn = 0, on = 0, on1 = 0, met = 0, met1 = 0, qn = 0, tiles = 0;   // phases met, tiles passed
-        // Tensor memory is read and written by whole warps, so they give up together: at
-        // once after wait(), at the end of the tile after the waits that every tile passes
-        // (a vote at each of those cost 32 tokens over 65568 e4m3 keys 3 us).
         bool ok = true;
         auto wait = [&](uint64_t *b, uint32_t parity) {
-            return ok = __all_sync(0xffffffffu, tc::mbar_wait(b, parity, kWaitNs));
+            if (!warp_wait(b, parity)) ok = false;
+            return ok;
         };
         auto meet = [&](int which, uint32_t parity) {    // both groups
             tc::mbar_arrive(&bar->meet[which]);
-            return wait(&bar->meet[which], parity);
+            // (long waits: lanes polling on their own and one vote disturb the other group less;
+            // 32 tokens over 32768 bf16 keys 41.8 us, with warp_wait 42.9)
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar->meet[which], parity, kWaitNs))) ok = false;
+            return ok;
         };
         Seg shared[2];                                   // the tiles shared with other CTAs
         int n_shared = 0;
         for (int sg = 0; ok; ++sg) {
-            const Seg *seg = open(sg);
-            if (!__all_sync(0xffffffffu, seg != nullptr)) {
+            const Seg *seg = &bar->seg[sg % kSegs];
+            if (!warp_wait(&bar->seg_full[sg % kSegs], (sg / kSegs) & 1)) {
                 ok = false;
                 break;
             }
@@ -740,7 +760,10 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const bool head = j < step;              // the group's first tile of the segment
                 if constexpr (E4) {
                     const uint32_t tile = tiles + j;
-                    if (!tc::mbar_wait(&bar->sc_full[tile % kScales], (tile / kScales) & 1, kWaitNs)) ok = false;
+                    if (!warp_wait(&bar->sc_full[tile % kScales], (tile / kScales) & 1)) {
+                        ok = false;
+                        break;
+                    }
                 }
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
@@ -753,7 +776,10 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             lv[i] = (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
                         }
                     }
-                    if (!tc::mbar_wait(&bar->s_full[gr][h], sn & 1, kWaitNs)) ok = false;
+                    if (!warp_wait(&bar->s_full[gr][h], sn & 1)) {
+                        ok = false;
+                        break;
+                    }
                     tc::tc_fence_after();
                     uint32_t s[HK];
                     const uint32_t sc = ts + (h == 0 ? a_col : a_col ^ HK);
@@ -835,12 +861,11 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                             // not implied by these scores (the first half's of a tile: both
                             // of the last tile's).  The first product overwrites O.
                             if (h == 0) {
-                                if (!(early & 1) && !tc::mbar_wait(&bar->pv_done[gr][0], (sn - 1) & 1, kWaitNs))
-                                    ok = false;
-                                if (!tc::mbar_wait(&bar->pv_done[gr][1], (sn - 1) & 1, kWaitNs)) ok = false;
+                                if (!(early & 1) && !warp_wait(&bar->pv_done[gr][0], (sn - 1) & 1)) ok = false;
+                                if (!warp_wait(&bar->pv_done[gr][1], (sn - 1) & 1)) ok = false;
                                 early = 3;
                             } else {
-                                if (!tc::mbar_wait(&bar->pv_done[gr][0], sn & 1, kWaitNs)) ok = false;
+                                if (!warp_wait(&bar->pv_done[gr][0], sn & 1)) ok = false;
                                 early |= 4;
                             }
                             tc::tc_fence_after();
@@ -861,15 +886,15 @@ attend_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         settled = true;
                     }
                     l += sum;
-                    if (!head && !(early >> h & 1) &&
-                        !tc::mbar_wait(&bar->pv_done[gr][h], (sn - 1) & 1, kWaitNs))
+                    if (!head && !(early >> h & 1) && !warp_wait(&bar->pv_done[gr][h], (sn - 1) & 1)) {
                         ok = false;
+                        break;
+                    }
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     tc::mbar_arrive(&bar->p_full[gr][h]);
                 }
                 early >>= 2;
-                ok = __all_sync(0xffffffffu, ok);
             }
             if (!ok) break;
             tiles += T;
@@ -1178,7 +1203,8 @@ cudaError_t tile_p(const AttendArgs &a, cudaStream_t s) {
     // Pairs of row tiles fetch (and convert) K and V once for 256 rows; single row tiles
     // are passed in half the time, by both groups, and make twice as many pieces of
     // work.  Those win while there is an SM for each row tile and little work an SM
-    // (as bounded by the batch), us for 8 kv heads of 6 query heads, d = 128:
+    // (as bounded by the batch: a call whose bounds are far above its lengths may get the
+    // other form, with the same results), us for 8 kv heads of 6 query heads, d = 128:
     //   tokens, keys     bf16 pair / single      e4m3 pair / single
     //   32, 1024              20.8 / 15.5            27.2 / 23.1
     //   32, 4096              21.6 / 17.8            26.4 / 22.7
@@ -1186,6 +1212,12 @@ cudaError_t tile_p(const AttendArgs &a, cudaStream_t s) {
     //   256, 2048             28.0 / 23.9            36.0 / 43.4
     //   256, 4096             36.1 / 39.4            46.5 / 72.9
     //   512, 1024             22.9 / 39.9            29.9 / 56.1
+    // d = 64:
+    //   32, 4096              18.1 / 15.6            21.6 / 18.1
+    //   256, 1024             19.9 / 14.0            24.4 / 17.4
+    //   256, 2048             23.9 / 20.1            28.1 / 26.3
+    //   256, 4096             31.5 / 33.3            37.9 / 44.1
+    //   512, 1024             20.1 / 34.5            25.0 / 41.7
     const int64_t of_seq = ((int64_t)a.b.max_q_len * a.gqa + TR - 1) / TR;
     const int64_t tiles =
         a.b.G * min(a.b.n_seqs * of_seq, (int64_t)a.b.n_tokens * a.gqa / TR + a.b.n_seqs);
