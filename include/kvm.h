@@ -67,7 +67,8 @@ typedef enum {
 /* Element types.  KVM_E4M3 is 8-bit floating point (1 sign, 4 exponent bits
  * with bias 7, 3 mantissa bits; no infinity, S.1111.111 is NaN; largest
  * finite value 448), the FP8 KV cache of the [KVMem] §6.1 platforms.  It is
- * for kv_dtype only, stored at unit scale; values written by the library are
+ * for kv_dtype only, stored at unit scale, or where kvm_cache or
+ * kvm_build_index_scaled are given scales, at theirs; values written by the library are
  * rounded to nearest even and saturate to +-448. */
 enum { KVM_F32 = 0, KVM_BF16 = 1, KVM_E4M3 = 2 };
 enum { KVM_DEVICE = 0, KVM_HOST_PINNED = 1 };    /* where a buffer lives     */
@@ -551,7 +552,8 @@ kvm_status kvm_append_kv(kvm_ctx *ctx, const kvm_batch *batch, const kvm_cache *
  * K / V were appended before.
  * q     device, q_dtype: token row i at q + i * q_stride elements, H heads of d
  *       (rotated; kvm_qk_norm_rope's q_rot).
- * out   device, q_dtype, token row i at out + i * out_stride elements.
+ * out   device, q_dtype, token row i at out + i * out_stride elements; its rows
+ *       do not overlap q's.
  * lse   nullable, device float32 [n_tokens][H].
  * Bases and strides multiples of 16 bytes; all buffers device memory.
  * softmax_scale is usually 1 / sqrt(d); at most 1e30 in magnitude.

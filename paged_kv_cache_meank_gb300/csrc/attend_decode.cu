@@ -22,10 +22,10 @@
 // a power of two per row, the page's k_scale goes into the factor of the scores
 // and the weights times v_scale, by a finite factor, have a reference of their own.
 //
-// One sequence of 32768 bf16 keys takes 26.9 us, 19.0 of them its 134 MB at the
+// One sequence of 32768 bf16 keys takes 26.8 us, 19.0 of them its 134 MB at the
 // 7.06 TB/s that longer sequences add; the start (lengths, page numbers and keys,
 // each read before the next can be) takes 5 and leaving and joining the parts 3.  24
-// ragged sequences of e4m3 pages (508 MB) take 90.1 us, 5.6 TB/s.
+// ragged sequences of e4m3 pages (508 MB) take 89.8 us, 5.7 TB/s.
 // Three 8 KB or four 4 KB stages a warp; eight to twelve warps an SM.  With fewer
 // tiles than SMs they are one CTA, for as few parts to join as can be: one
 // sequence of 32768 bf16 keys took 27.4 us against 31.4 with two CTAs of four
@@ -48,8 +48,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Pages of a CTA's run at least, and what a join costs.  One sequence of 512, 1024,
-// 2048, 4096 bf16 keys took 6.3, 9.0, 9.4, 9.0 us with 8 and 16; with 4 and 8, 7.6, 7.8,
-// 8.3, 9.2.
+// 2048, 4096 bf16 keys takes 6.2, 7.6, 8.2, 9.2 us; with 8 and 16 it took 6.3, 9.0, 9.4,
+// 9.0, with 4 and 8, 7.6, 7.8, 8.3, 9.2.
 constexpr int kMinPages = 4, kJoinPages = 16;
 
 // W warps a CTA, CTAS of them an SM.

@@ -12,6 +12,8 @@
 // pairs, a lane 8 codes of a half row and their rotate-half partners.  Bound by
 // HBM: 32 d bytes read and 32 d written (raw K) a pair.  256 blocks of 64 layers
 // and 8 kv heads, d = 128 (1.11 GB), take 187 us, 5.9 TB/s; one block takes 5.9 us.
+// Without raw K half the bytes are left and nearly all of the arithmetic: 130 us, bound by
+// its issue.
 #include "kvm_internal.cuh"
 #include "kvm_vec.cuh"
 
