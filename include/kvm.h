@@ -531,8 +531,8 @@ kvm_status kvm_qk_norm_rope(kvm_ctx *ctx, int32_t n_tokens, const int32_t *posit
  * infinity times a sine of 0 is NaN.
  * A block to be continued whose k_scale or v_scale so far is no such power of two
  * raises the device error flag; its head's codes and scales are left as they were.
- * Each page written belongs to one sequence of the batch; a sequence with
- * kv_len < q_len raises the device error flag and is skipped.
+ * Each page written, and its scale row, belongs to one block of one sequence of the
+ * batch; a sequence with kv_len < q_len raises the device error flag and is skipped.
  * Errors: KVM_ERR_INVALID_ARG; KVM_ERR_CAPACITY for more than 1024 sequences or
  * n_seqs * max_q_len beyond about 2^36.
  */
